@@ -18,14 +18,14 @@ LIB_PATH = os.path.join(_PKG, "libfp4kv.so")
 
 KEY_BF16, KEY_E4M3, KEY_E2M1 = 0, 1, 2
 OP_KV_QUANT, OP_INDEXER_TOPK, OP_REINDEX_TOPK, OP_HIER_POOL_SELECT, OP_SPARSE_ATTN, \
-    OP_INDEXER_SCORES = range(6)
+    OP_INDEXER_SCORES, OP_TREE_ATTN = range(7)
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA",
                 4: "WORKSPACE_TOO_SMALL", 5: "DEVICE_FLAG"}
 
 # (name, restype, argtypes) of every exported symbol
-_P, _I32, _I64, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, \
-    ctypes.c_float
+_P, _I32, _I64, _SZ, _F32, _F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, \
+    ctypes.c_float, ctypes.c_double
 SIGNATURES = [
     ("fp4kv_last_error", ctypes.c_char_p, []),
     ("fp4kv_version", ctypes.c_char_p, []),
@@ -52,6 +52,11 @@ SIGNATURES = [
     ("fp4kv_topk_merge", ctypes.c_int, [_P, _P, _I32, _I32, _I32, ctypes.POINTER(_I32), _I32, _I32, _I32, _P,
                                         _P, _P, _P]),
     ("fp4kv_lse_combine", ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    ("fp4kv_qkv_norm_rope_fp4", ctypes.c_int,
+     [_P, _I64, _I64, _I32, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _F64, _P]),
+    ("fp4kv_kv_dequant_fp4", ctypes.c_int, [_P, _P, _I64, _I32, _P, _I64, _P, _I32, _I64, _P]),
+    ("fp4kv_tree_attn_decode", ctypes.c_int,
+     [_P, _I32, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _I32, _F32, _P, _P, _P, _SZ, _P]),
     ("fp4kv_noalloc_status", ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
     ("fp4kv_selftest_wait_timeout_noalloc", ctypes.c_int, [_I32, _P]),
 ]
@@ -343,6 +348,174 @@ def swa_quant_fp8(x: torch.Tensor, out: torch.Tensor, dst_row: torch.Tensor | No
         _need(dst_row, torch.int64, "dst_row", x.device)
     _check(lib().fp4kv_swa_quant_fp8(_ptr(x), n, d, x.stride(0), _ptr(dst_row), _ptr(out), cap,
                                      _stream(x.device)))
+
+
+def _call(fn, dev, *args):
+    """A library call with dev as the current device, on dev's current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_of(packed, scales, d, dev):
+    """Rows of a cache given as contiguous uint8 planes [..., d/2] and [..., d/16]."""
+    _need(packed, torch.uint8, "packed", dev)
+    _need(scales, torch.uint8, "scales", dev)
+    cap = packed.numel() // (d // 2)
+    if packed.numel() != cap * (d // 2) or scales.numel() != cap * (d // 16):
+        raise ValueError("packed / scales do not match d")
+    return cap
+
+
+def qkv_norm_rope_fp4(q, kv, *, positions=None, cos_sin=None, rope_dim=0, rope_half=False, q_weight=None, kv_weight=None,
+                      eps=1e-6, q_out=None, kv_out=None, packed=None, scales=None, dst_row=None):
+    """RMS norm and rotation of the query heads q bf16 [n, H, d] and of the KV rows kv bf16
+    [n, d] (either may be None; unit channel stride, other strides free), in one launch, with
+    the KV rows' write to the FP4 cache (packed [cap, d/2], scales [cap, d/16], at rows
+    dst_row int64 [n] or 0..n-1). The last rope_dim channels are rotated in neighbouring pairs
+    (rope_half: pairs rope_dim / 2 apart) by row positions[i] of cos_sin fp32 [max_pos,
+    rope_dim] (cosines, then sines). Returns (q_out bf16 [n, H, d], kv_out bf16 [n, d]); kv_out
+    is made only where it is given or there is no cache to write to."""
+    one = kv if q is None else q
+    if one is None:
+        raise ValueError("q or kv is required")
+    dev, n, d = one.device, one.shape[0], one.shape[-1]
+    for t, name, dim in ((q, "q", 3), (kv, "kv", 2)):
+        if t is not None:
+            _need(t, torch.bfloat16, name, dev, contiguous=False)
+            if t.dim() != dim or t.shape[0] != n or t.shape[-1] != d or (t.stride(-1) != 1 and t.numel()):
+                raise ValueError("q [n, H, d] and kv [n, d] with unit channel stride expected")
+    H = 0 if q is None else q.shape[1]
+    for t, name in ((q_weight, "q_weight"), (kv_weight, "kv_weight")):
+        if t is not None:
+            _need(t, torch.bfloat16, name, dev)
+            if t.numel() != d:
+                raise ValueError(f"{name}: expected d = {d} values")
+    max_pos = 0
+    if rope_dim:
+        _need(positions, torch.int64, "positions", dev)
+        _need(cos_sin, torch.float32, "cos_sin", dev)
+        if positions.numel() != n or cos_sin.dim() != 2 or cos_sin.shape[1] != rope_dim:
+            raise ValueError("positions [n] and cos_sin [max_pos, rope_dim] expected")
+        max_pos = cos_sin.shape[0]
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty((n, H, d), dtype=torch.bfloat16, device=dev)
+        _need(q_out, torch.bfloat16, "q_out", dev)
+        if q_out.numel() != n * H * d:
+            raise ValueError("q_out: expected [n, H, d]")
+    cap = 0
+    if kv is None:
+        if packed is not None or scales is not None or kv_out is not None:
+            raise ValueError("packed, scales and kv_out need kv")
+    else:
+        if packed is not None or scales is not None:
+            cap = _rows_of(packed, scales, d, dev)
+            if dst_row is not None:
+                _need(dst_row, torch.int64, "dst_row", dev)
+                if dst_row.numel() != n:
+                    raise ValueError("dst_row: expected [n]")
+        elif kv_out is None:
+            kv_out = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+        if kv_out is not None:
+            _need(kv_out, torch.bfloat16, "kv_out", dev)
+            if kv_out.numel() != n * d:
+                raise ValueError("kv_out: expected [n, d]")
+    if n == 0:
+        return q_out, kv_out
+    _call(lib().fp4kv_qkv_norm_rope_fp4, dev, _addr(q), 0 if q is None else _stride(q, 0, H * d),
+          0 if q is None else _stride(q, 1, d), H, _addr(q_weight), _addr(q_out) if q is not None else None, _addr(kv),
+          0 if kv is None else _stride(kv, 0, d), _addr(kv_weight), _addr(kv_out), _addr(dst_row), _addr(packed),
+          _addr(scales), cap, n, d, rope_dim, 1 if rope_half else 0, _addr(positions) if rope_dim else None,
+          _addr(cos_sin) if rope_dim else None, max_pos, eps)
+    return q_out, kv_out
+
+
+def _stride(t, dim, alone):
+    """The stride of a dimension; one of a single entry, whose stride means nothing, counts as `alone`."""
+    return alone if t.shape[dim] == 1 else t.stride(dim)
+
+
+def kv_dequant_fp4(packed, scales, src_row=None, out=None, dtype=torch.bfloat16):
+    """Rows of the FP4 cache packed [..., d/2], scales [..., d/16] as bf16 or fp32 (out's type,
+    else dtype): row src_row[i] (int64 [n]; rows outside the cache give zeros), or every row in
+    order. Exact. out [n, d] may have a row stride above d. Returns out."""
+    _need(packed, torch.uint8, "packed")
+    dev, d = packed.device, 2 * packed.shape[-1]
+    cap = _rows_of(packed, scales, d, dev)
+    n = cap
+    if src_row is not None:
+        _need(src_row, torch.int64, "src_row", dev)
+        n = src_row.numel()
+    if out is None:
+        out = torch.empty((n, d), dtype=dtype, device=dev)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out: expected bf16 or fp32, got {out.dtype}")
+    _need(out, out.dtype, "out", dev, contiguous=False)
+    if out.dim() != 2 or out.shape[0] != n or out.shape[1] != d or (out.stride(1) != 1 and out.numel()):
+        raise ValueError("out: expected [n, d] with unit channel stride")
+    if n:
+        _call(lib().fp4kv_kv_dequant_fp4, dev, packed.data_ptr(), scales.data_ptr(), cap, d, _addr(src_row), n,
+              out.data_ptr(), 1 if out.dtype == torch.float32 else 0, _stride(out, 0, d))
+    return out
+
+
+def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None, idx=None, sm_scale=1.0, ws=None,
+                     out=None, lse=None, want_lse=True):
+    """Attention of T drafted tokens per sequence, a tree, over the FP4 cache: q bf16 [B, T, H,
+    512]; packed uint8 [B, cap, 256]; scales uint8 [B, cap, 32]; prefix_lens int32 [B];
+    tree_mask int64 [B, T] (bit j: the token sees draft j, whose row is prefix_lens + j);
+    n_draft (optional) int32 [B]; idx (optional) int32 [B, top_k]: the prefix positions to
+    attend (every one without it). Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
+    None); tokens behind n_draft keep what their outputs held."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 4:
+        raise ValueError("q: expected [B, T, H, d]")
+    dev = q.device
+    B, T, H, d = q.shape
+    _need(packed, torch.uint8, "packed", dev)
+    _need(scales, torch.uint8, "scales", dev)
+    cap = packed.shape[1]
+    if packed.shape != (B, cap, d // 2) or scales.shape != (B, cap, d // 16):
+        raise ValueError("packed [B, cap, d/2] and scales [B, cap, d/16] expected")
+    _need(prefix_lens, torch.int32, "prefix_lens", dev)
+    _need(tree_mask, torch.int64, "tree_mask", dev)
+    if prefix_lens.numel() != B or tree_mask.shape != (B, T):
+        raise ValueError("prefix_lens [B] and tree_mask [B, T] expected")
+    if n_draft is not None:
+        _need(n_draft, torch.int32, "n_draft", dev)
+        if n_draft.numel() != B:
+            raise ValueError("n_draft: expected [B]")
+    top_k = 0
+    if idx is not None:
+        _need(idx, torch.int32, "idx", dev)
+        if idx.dim() != 2 or idx.shape[0] != B:
+            raise ValueError("idx: expected [B, top_k]")
+        top_k = idx.shape[1]
+    if out is None:
+        out = torch.zeros((B, T, H, d), dtype=torch.bfloat16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.full((B, T, H), float("-inf"), dtype=torch.float32, device=dev)
+    _need(out, torch.bfloat16, "out", dev)
+    if out.shape != q.shape:
+        raise ValueError("out: expected q's shape")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", dev)
+        if lse.shape != (B, T, H):
+            raise ValueError("lse: expected [B, T, H]")
+    if ws is None:
+        ws = alloc_workspace(workspace_bytes(OP_TREE_ATTN, B, cap, T * H, top_k), dev)
+    _need(ws, torch.uint8, "ws", dev)
+    _call(lib().fp4kv_tree_attn_decode, dev, q.data_ptr(), B, T, H, d, packed.data_ptr(), scales.data_ptr(), cap,
+          prefix_lens.data_ptr(), _addr(n_draft), tree_mask.data_ptr(), _addr(idx), top_k, sm_scale, out.data_ptr(),
+          _addr(lse), ws.data_ptr(), ws.numel())
+    return out, lse
 
 
 def profile_enable(on: bool = True):

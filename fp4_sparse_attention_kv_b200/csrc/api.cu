@@ -168,6 +168,16 @@ AttnLayout attn_layout(int64_t B, int64_t H, int64_t top_k, int sms) {
   return L;
 }
 
+struct TreeLayout {
+  size_t total = kAlign;  // status word
+};
+
+// rows: T * H query rows per sequence; top_k 0: every row of the prefix is attended
+TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int sms) {
+  (void)B, (void)rows, (void)cap, (void)top_k, (void)sms;
+  return TreeLayout{};
+}
+
 // ---------------------------------------------------------------------------------------
 // Shared validation of the indexer query / key arguments
 // ---------------------------------------------------------------------------------------
@@ -256,6 +266,9 @@ size_t fp4kv_workspace_bytes(int32_t op, int32_t B, int64_t cap, int32_t heads, 
       return attn_layout(B, heads, top_k, num_sms()).total;
     case FP4KV_OP_INDEXER_SCORES:
       return indexer_layout(3, B, cap, top_k, n_pool_blocks).total;
+    case FP4KV_OP_TREE_ATTN:
+      if (heads < 1 || top_k < 0) return 0;
+      return tree_layout(B, heads, cap, top_k, num_sms()).total;
     default:
       return 0;
   }
@@ -576,6 +589,140 @@ fp4kv_status fp4kv_sparse_swa_attn_decode(const uint16_t* q, int32_t B, int32_t 
   if (!aligned(swa, 16)) return fail(FP4KV_ERR_INVALID_ARG, "swa must be 16-byte aligned");
   return run_attn(q, B, H, d, packed, scales, cap, seq_lens, idx, top_k, swa, n_win, sm_scale, out, lse,
                   ws, ws_bytes, stream);
+}
+
+fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, int64_t q_head_stride, int32_t H,
+                                     const uint16_t* q_weight, uint16_t* q_out, const uint16_t* kv,
+                                     int64_t kv_row_stride, const uint16_t* kv_weight, uint16_t* kv_out,
+                                     const int64_t* dst_row, uint8_t* packed, uint8_t* scales, int64_t cap_rows,
+                                     int64_t n_tokens, int32_t d, int32_t rope_dim, int32_t rope_half,
+                                     const int64_t* positions, const float* cos_sin, int64_t max_pos, double eps,
+                                     void* stream) {
+  if (n_tokens < 0 || cap_rows < 0 || max_pos < 0)
+    return fail(FP4KV_ERR_INVALID_ARG, "negative n_tokens, cap_rows or max_pos");
+  if (n_tokens > (int64_t(1) << 31)) return fail(FP4KV_ERR_UNSUPPORTED, "n_tokens=%lld above 2^31", (long long)n_tokens);
+  if (d % 32 != 0 || d < 32 || d > 1024) return fail(FP4KV_ERR_UNSUPPORTED, "d=%d must be a multiple of 32 in [32, 1024]", d);
+  if (rope_dim % 16 != 0 || rope_dim < 0 || rope_dim > d)
+    return fail(FP4KV_ERR_UNSUPPORTED, "rope_dim=%d must be a multiple of 16 in [0, d]", rope_dim);
+  if (!(eps >= 1e-30 && eps < 1e30)) return fail(FP4KV_ERR_INVALID_ARG, "eps=%g outside [1e-30, 1e30)", eps);
+  if (!q && !kv) return fail(FP4KV_ERR_INVALID_ARG, "null q and kv");
+  if (q && (H < 1 || H > 128)) return fail(FP4KV_ERR_UNSUPPORTED, "H=%d outside [1, 128]", H);
+  if (n_tokens == 0) return ok();
+  if (q && !q_out) return fail(FP4KV_ERR_INVALID_ARG, "null q_out");
+  if (kv && !kv_out && !packed) return fail(FP4KV_ERR_INVALID_ARG, "kv has neither kv_out nor packed to go to");
+  if (packed && !(kv && scales)) return fail(FP4KV_ERR_INVALID_ARG, "packed needs kv and scales");
+  if (rope_dim && (!positions || !cos_sin)) return fail(FP4KV_ERR_INVALID_ARG, "null positions or cos_sin with rope_dim > 0");
+  if (q && (q_head_stride < d || q_head_stride % 8 || q_tok_stride < d || q_tok_stride % 8))
+    return fail(FP4KV_ERR_INVALID_ARG, "q strides (%lld, %lld) must be >= d and multiples of 8", (long long)q_tok_stride,
+                (long long)q_head_stride);
+  if (kv && (kv_row_stride < d || kv_row_stride % 8))
+    return fail(FP4KV_ERR_INVALID_ARG, "kv_row_stride=%lld must be >= d and a multiple of 8", (long long)kv_row_stride);
+  if (!aligned(q, 16) || !aligned(q_weight, 16) || !aligned(q_out, 16) || !aligned(kv, 16) || !aligned(kv_weight, 16) ||
+      !aligned(kv_out, 16) || !aligned(cos_sin, 16) || !aligned(packed, 8) || !aligned(positions, 8) ||
+      !aligned(dst_row, 8))
+    return fail(FP4KV_ERR_INVALID_ARG,
+                "q, kv, weights, outputs and cos_sin must be 16-byte, packed, positions and dst_row 8-byte aligned");
+  if (packed && !dst_row && n_tokens > cap_rows)
+    return fail(FP4KV_ERR_INVALID_ARG, "n_tokens > cap_rows with dst_row == NULL");
+  fp4kv::NormRopeParams p{};
+  p.q = q;
+  p.q_tok_stride = q_tok_stride;
+  p.q_head_stride = q_head_stride;
+  p.H = q ? H : 0;
+  p.q_weight = q_weight;
+  p.q_out = q_out;
+  p.kv = kv;
+  p.kv_stride = kv_row_stride;
+  p.kv_weight = kv_weight;
+  p.kv_out = kv_out;
+  p.dst_row = dst_row;
+  p.packed = packed;
+  p.scales = scales;
+  p.cap_rows = cap_rows;
+  p.n_tokens = n_tokens;
+  p.d = d;
+  p.rope_dim = rope_dim;
+  p.rope_half = rope_half != 0;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.eps = eps;
+  cudaError_t e;
+  {
+    prof::Scope ps(0, static_cast<cudaStream_t>(stream));
+    e = fp4kv::launch_qkv_norm_rope(p, static_cast<cudaStream_t>(stream));
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "qkv_norm_rope_fp4");
+  return ok();
+}
+
+fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, int64_t cap_rows, int32_t d,
+                                  const int64_t* src_row, int64_t n_rows, void* out, int32_t out_f32,
+                                  int64_t out_row_stride, void* stream) {
+  if (n_rows < 0 || cap_rows < 0) return fail(FP4KV_ERR_INVALID_ARG, "negative n_rows or cap_rows");
+  if (d % 32 != 0 || d < 32 || d > 1024) return fail(FP4KV_ERR_UNSUPPORTED, "d=%d must be a multiple of 32 in [32, 1024]", d);
+  if (n_rows == 0) return ok();
+  if (!packed || !scales || !out) return fail(FP4KV_ERR_INVALID_ARG, "null packed, scales or out");
+  if (out_row_stride < d || out_row_stride % (out_f32 ? 4 : 8) != 0)
+    return fail(FP4KV_ERR_INVALID_ARG, "out_row_stride=%lld must be >= d and a multiple of 16 bytes", (long long)out_row_stride);
+  if (!aligned(packed, 16) || !aligned(out, 16) || !aligned(src_row, 8))
+    return fail(FP4KV_ERR_INVALID_ARG, "packed and out must be 16-byte and src_row 8-byte aligned");
+  if (!src_row && n_rows > cap_rows) return fail(FP4KV_ERR_INVALID_ARG, "n_rows > cap_rows with src_row == NULL");
+  cudaError_t e;
+  {
+    prof::Scope ps(0, static_cast<cudaStream_t>(stream));
+    e = fp4kv::launch_kv_dequant_fp4(packed, scales, cap_rows, d, src_row, n_rows, out, out_f32 != 0, out_row_stride,
+                                     num_sms(), static_cast<cudaStream_t>(stream));
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "kv_dequant_fp4");
+  return ok();
+}
+
+fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int32_t H, int32_t d,
+                                    const uint8_t* packed, const uint8_t* scales, int64_t cap,
+                                    const int32_t* prefix_lens, const int32_t* n_draft, const uint64_t* tree_mask,
+                                    const int32_t* idx, int32_t top_k, float sm_scale, uint16_t* out, float* lse,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  if (!q || !packed || !scales || !prefix_lens || !tree_mask || !out || !ws)
+    return fail(FP4KV_ERR_INVALID_ARG, "null pointer argument");
+  if (B < 1 || B > 65535) return fail(FP4KV_ERR_UNSUPPORTED, "B=%d outside [1, 65535]", B);
+  if (T < 1 || T > 64) return fail(FP4KV_ERR_UNSUPPORTED, "T=%d outside [1, 64]", T);
+  if (H < 1 || H > 128) return fail(FP4KV_ERR_UNSUPPORTED, "H=%d outside [1, 128]", H);
+  if (d != 512) return fail(FP4KV_ERR_UNSUPPORTED, "d=%d (attention is built for d=512)", d);
+  if (idx ? (top_k < 1 || top_k > (1 << 20)) : top_k != 0)
+    return fail(FP4KV_ERR_UNSUPPORTED, "top_k=%d (1 .. 2^20 with idx, 0 without)", top_k);
+  if (cap < 1 || cap > (int64_t(1) << 31) - 8)
+    return fail(FP4KV_ERR_UNSUPPORTED, "cap=%lld outside [1, 2^31 - 8]", (long long)cap);
+  if (!aligned(q, 16) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(out, 16) || !aligned(tree_mask, 8) ||
+      !aligned(idx, 4) || !aligned(ws, kAlign))
+    return fail(FP4KV_ERR_INVALID_ARG, "misaligned q/packed/scales/out (16 B), tree_mask (8 B) or ws (256 B)");
+  const int sms = num_sms();
+  const TreeLayout L = tree_layout(B, int64_t(T) * H, cap, top_k, sms);
+  if (ws_bytes < L.total) return fail(FP4KV_ERR_WORKSPACE_TOO_SMALL, "ws_bytes %zu < %zu", ws_bytes, L.total);
+  fp4kv::TreeAttnParams p{};
+  p.q = q;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.packed = packed;
+  p.scales = scales;
+  p.cap = cap;
+  p.prefix_lens = prefix_lens;
+  p.n_draft = n_draft;
+  p.tree_mask = tree_mask;
+  p.idx = idx;
+  p.top_k = top_k;
+  p.sm_scale = sm_scale;
+  p.out = out;
+  p.lse = lse;
+  p.status = static_cast<uint32_t*>(ws);
+  cudaError_t e;
+  {
+    prof::Scope ps(3, static_cast<cudaStream_t>(stream));
+    e = fp4kv::launch_tree_attn(p, sms, static_cast<cudaStream_t>(stream));
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "tree_attn_decode");
+  return ok();
 }
 
 // ---------------------------------------------------------------------------------------

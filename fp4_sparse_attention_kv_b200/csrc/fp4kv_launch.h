@@ -13,6 +13,35 @@ cudaError_t launch_swa_quant_fp8(const uint16_t* x, int64_t n_rows, int d, int64
                                  const int64_t* dst_row, uint8_t* out, int64_t cap_rows, int num_sms,
                                  cudaStream_t stream);
 
+cudaError_t launch_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, int64_t cap_rows, int d,
+                                  const int64_t* src_row, int64_t n_rows, void* out, bool f32, int64_t out_row_stride,
+                                  int num_sms, cudaStream_t stream);
+
+// RMS norm and rotation of query heads and KV rows, with the FP4 write of the KV rows.
+struct NormRopeParams {
+  const uint16_t* q;         // nullable: head h of token i at q + i * q_tok_stride + h * q_head_stride
+  int64_t q_tok_stride, q_head_stride;
+  int H;
+  const uint16_t* q_weight;  // nullable [d]
+  uint16_t* q_out;           // [n_tokens][H][d]
+  const uint16_t* kv;        // nullable: row i at kv + i * kv_stride
+  int64_t kv_stride;
+  const uint16_t* kv_weight; // nullable [d]
+  uint16_t* kv_out;          // nullable [n_tokens][d]
+  const int64_t* dst_row;    // nullable: cache row of each token (i)
+  uint8_t* packed;           // nullable [cap_rows][d/2]
+  uint8_t* scales;           // [cap_rows][d/16]
+  int64_t cap_rows;
+  int64_t n_tokens;
+  int d, rope_dim;
+  bool rope_half;            // pairs (j, j + rope_dim / 2) instead of (2j, 2j + 1)
+  const int64_t* positions;  // [n_tokens]
+  const float* cos_sin;      // [max_pos][rope_dim]: cosines, then sines
+  int64_t max_pos;
+  double eps;
+};
+cudaError_t launch_qkv_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+
 // ----------------------------------------------------------------------------------------
 // Indexer scoring (Full scan or pool gather), fused with the first-level histogram of the
 // top-K select and, for the hierarchical Full layer, the block max over 8 positions.
@@ -98,6 +127,27 @@ struct AttnParams {
   uint32_t* status;
 };
 cudaError_t launch_sparse_attn(const AttnParams& p, int num_sms, cudaStream_t stream);
+
+// ----------------------------------------------------------------------------------------
+// Attention of a tree of drafted tokens over the cache
+// ----------------------------------------------------------------------------------------
+struct TreeAttnParams {
+  const uint16_t* q;          // [B][T][H][512] bf16
+  int B, T, H;
+  const uint8_t* packed;      // [B][cap][256]
+  const uint8_t* scales;      // [B][cap][32]
+  int64_t cap;
+  const int32_t* prefix_lens; // [B]
+  const int32_t* n_draft;     // nullable [B]
+  const uint64_t* tree_mask;  // [B][T]: bit j: token sees draft j
+  const int32_t* idx;         // nullable [B][top_k]
+  int top_k;
+  float sm_scale;
+  uint16_t* out;              // [B][T][H][512] bf16
+  float* lse;                 // nullable [B][T][H]
+  uint32_t* status;
+};
+cudaError_t launch_tree_attn(const TreeAttnParams& p, int num_sms, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------------------
 // Context-sharded decode: exact merge of per-range top-K candidates, and the log-sum-exp

@@ -24,50 +24,13 @@
 // four rows' loads in flight per warp; otherwise one warp per row, one 16-channel group per
 // lane (32 B read, 8 B + 1 B written per lane).
 #include "fp4kv_common.cuh"
+#include "fp4kv_quant.cuh"
 #include "fp4kv_sm100.cuh"
 #include "fp4kv_launch.h"
 
 namespace fp4kv {
 
 namespace {
-
-// RN(a * inv + 128) - 128: the ratio a * inv rounded once to a multiple of 2^-16 (for
-// a * inv < 128; larger ratios saturate the code either way)
-FP4KV_DEV float snap_ratio(float a, float inv) {
-  return __fadd_rn(__fmaf_rn(a, inv, 128.0f), -128.0f);
-}
-
-// Quantize one group of 16 bf16 values held as 8 words (2 values per word, low half first).
-// Returns the 8 packed bytes (low nibble = even channel) and the scale code.
-FP4KV_DEV void quant_group(const uint32_t (&w)[8], uint2& packed, uint32_t& scale_code) {
-  uint32_t m2 = 0;  // per-half maxima of the 15-bit magnitudes
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7fff7fffu);
-  const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
-  const float amax = bf16_bits_to_f32(m);
-  const uint32_t sc = f32_to_e4m3_satfinite(__fdiv_rn(amax, 6.0f));
-  const float S = f16_lo_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(sc)));
-  uint32_t bytes[8];
-  if (S > 0.0f) {
-    const float inv = __frcp_rn(S);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t e = w[i] << 16, o = w[i] & 0xffff0000u;  // the two channels as f32 bits
-      const float r0 = snap_ratio(__uint_as_float(e & 0x7fffffffu), inv);
-      const float r1 = snap_ratio(__uint_as_float(o & 0x7fffffffu), inv);
-      // the sign goes back on before the rounding to E2M1, which is symmetric; a negative
-      // value that rounds to zero keeps its sign (code 0x8)
-      bytes[i] = f32x2_to_e2m1x2_satfinite(__uint_as_float(__float_as_uint(r0) | (e & 0x80000000u)),
-                                           __uint_as_float(__float_as_uint(r1) | (o & 0x80000000u)));
-    }
-  } else {  // an all-zero group: sign-only codes
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bytes[i] = ((w[i] >> 12) & 0x8u) | ((w[i] >> 24) & 0x80u);
-  }
-  packed.x = bytes[0] | (bytes[1] << 8) | (bytes[2] << 16) | (bytes[3] << 24);
-  packed.y = bytes[4] | (bytes[5] << 8) | (bytes[6] << 16) | (bytes[7] << 24);
-  scale_code = sc;
-}
 
 __global__ void __launch_bounds__(256) k_kv_quant_fp4(const uint16_t* __restrict__ x,
                                                       int64_t n_rows, int d, int64_t x_stride,
@@ -185,23 +148,6 @@ __global__ void __launch_bounds__(256) k_swa_quant_fp8(const uint16_t* __restric
       *reinterpret_cast<uint4*>(orow + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
-}
-
-// A launch that may begin while the kernel before it on the stream finishes (programmatic
-// dependent launch); the kernel orders itself with griddep_wait().
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
 }  // namespace

@@ -81,7 +81,8 @@ typedef enum {
   FP4KV_OP_REINDEX_TOPK = 2,     /* fp4kv_indexer_topk with a pool */
   FP4KV_OP_HIER_POOL_SELECT = 3,
   FP4KV_OP_SPARSE_ATTN = 4,
-  FP4KV_OP_INDEXER_SCORES = 5
+  FP4KV_OP_INDEXER_SCORES = 5,
+  FP4KV_OP_TREE_ATTN = 6         /* heads: T * H query rows per sequence; top_k 0: no idx */
 } fp4kv_op;
 
 /* Supported ranges (anything else returns FP4KV_ERR_UNSUPPORTED):
@@ -251,6 +252,73 @@ fp4kv_status fp4kv_lse_combine(const float* part_out, const float* part_lse, int
 fp4kv_status fp4kv_swa_quant_fp8(const uint16_t* x, int64_t n_rows, int32_t d, int64_t x_row_stride,
                                  const int64_t* dst_row, uint8_t* out, int64_t cap_rows, void* stream);
 
+/* qkv_norm_rope_fp4 -- RMS norm and position rotation of a token's query heads and of its KV
+ * row in one launch; the KV row goes to the FP4 cache as it is made. (The pages do not say how
+ * queries and rows are normed and rotated: this is the form that latent attention needs.) For
+ * a row x of d channels with weight w (1 where NULL):
+ *   r = 1 / sqrt(sum x^2 / d + eps),  u = x * w;
+ *   the first d - rope_dim channels:  y_i = u_i * r;
+ *   the last rope_dim in pairs (a, b) with the token's (c, s): y_a = (u_a c - u_b s) * r,
+ *   y_b = (u_b c + u_a s) * r. The pairs are neighbours (2j, 2j + 1), or with rope_half != 0
+ *   (j, j + rope_dim / 2), counted from channel d - rope_dim.
+ * Queries are computed in fp32 and rounded once to bf16. The KV row is rounded to bf16 from a
+ * value good to 64 bits (kv_out, nullable), and that bf16 row is quantized exactly as
+ * fp4kv_kv_quant_fp4 does (packed / scales, nullable with kv_out given).
+ * q         : nullable bf16; head h of token i at q + i * q_tok_stride + h * q_head_stride.
+ * q_out     : bf16 [n_tokens][H][d]; may be q itself where q is contiguous.
+ * kv        : nullable bf16 rows [n_tokens][kv_row_stride]. kv_out: bf16 [n_tokens][d]; may be
+ *             kv itself where kv_row_stride == d.
+ * q_weight, kv_weight : nullable bf16 [d].
+ * dst_row   : nullable int64 [n_tokens]: the token's cache row (NULL: i). Rows outside
+ *             [0, cap_rows) are skipped (kv_out is still written). No row twice.
+ * positions : int64 [n_tokens]; cos_sin: fp32 [max_pos][rope_dim], a position's cosines
+ *             (rope_dim / 2), then its sines. Both unused with rope_dim == 0. A token whose
+ *             position lies outside [0, max_pos) is skipped: all its outputs stay as they were.
+ * d % 32 == 0, d <= 1024; rope_dim % 16 == 0, rope_dim <= d; 1 <= H <= 128; eps in
+ * [1e-30, 1e30). q, kv, the weights, the outputs and cos_sin are 16-byte aligned, strides
+ * multiples of 8. */
+fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, int64_t q_head_stride, int32_t H,
+                                     const uint16_t* q_weight, uint16_t* q_out, const uint16_t* kv,
+                                     int64_t kv_row_stride, const uint16_t* kv_weight, uint16_t* kv_out,
+                                     const int64_t* dst_row, uint8_t* packed, uint8_t* scales, int64_t cap_rows,
+                                     int64_t n_tokens, int32_t d, int32_t rope_dim, int32_t rope_half,
+                                     const int64_t* positions, const float* cos_sin, int64_t max_pos, double eps,
+                                     void* stream);
+
+/* kv_dequant_fp4 -- read-back of cache rows: the inverse of fp4kv_kv_quant_fp4 (no counterpart
+ * on the pages beside "dequantized before attention"). out row i = the values of cache row
+ * src_row[i] (NULL: row i), e2m1(code) * e4m3(scale): at most 6 significant bits, so exact in
+ * both output types. Rows outside [0, cap_rows) (the -1 of a selection) give zeros.
+ * out: bf16 (out_f32 == 0) or fp32 rows [n_rows][out_row_stride], 16-byte aligned, the row
+ * stride a multiple of 16 bytes. d % 32 == 0, d <= 1024. */
+fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, int64_t cap_rows, int32_t d,
+                                  const int64_t* src_row, int64_t n_rows, void* out, int32_t out_f32,
+                                  int64_t out_row_stride, void* stream);
+
+/* tree_attn_decode -- attention of a tree of drafted tokens (speculative decoding's
+ * verification; no counterpart on the pages). Sequence b has a prefix of prefix_lens[b]
+ * cache rows; its T drafted tokens' rows lie behind it, token j's at position
+ * prefix_lens[b] + j. Token t attends, in one softmax,
+ *   - the prefix: every row, or with idx the positions idx[b][0 .. top_k) that lie in
+ *     [0, prefix_lens[b]) (others, -1 among them, are absent; a position given twice counts
+ *     twice); and
+ *   - the drafted rows j whose bit j of tree_mask[b][t] is set (its own bit included: a mask
+ *     without it leaves the token's own row out).
+ * q [B][T][H][512] bf16; out the same shape, bf16; lse (nullable) fp32 [B][T][H] as in
+ * fp4kv_sparse_attn_decode. packed [B][cap][256], scales [B][cap][32]. n_draft (nullable)
+ * int32 [B]: sequence b drafts only its first n_draft[b] (clamped to [0, T]) tokens; q, mask
+ * and outputs of the others are not touched, and mask bits at or above it are ignored. Prefix
+ * lengths are clamped to [0, cap]; drafted rows at or behind cap are absent. A token that sees
+ * nothing gets out = 0, lse = -inf. A row that no token sees is not read.
+ * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without. ws: at least
+ * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,
+ * initialised once. q, packed, scales and out 16-byte aligned. */
+fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int32_t H, int32_t d,
+                                    const uint8_t* packed, const uint8_t* scales, int64_t cap,
+                                    const int32_t* prefix_lens, const int32_t* n_draft, const uint64_t* tree_mask,
+                                    const int32_t* idx, int32_t top_k, float sm_scale, uint16_t* out, float* lse,
+                                    void* ws, size_t ws_bytes, void* stream);
+
 /* indexer_topk_noalloc -- fp4kv_indexer_topk without a caller workspace. (The pages have
  * no counterpart: this is an integration aid.) For callers that cannot allocate device
  * memory: code inside a host runtime that owns all device memory (a serving engine with a
@@ -292,7 +360,8 @@ fp4kv_status fp4kv_selftest_wait_timeout_noalloc(int32_t limit_us, void* stream)
 /* Benchmark support (no counterpart on the pages). While enabled, every kernel the library
  * launches is bracketed by two CUDA events recorded on the launch stream (do not enable
  * during CUDA-graph capture). fp4kv_profile_read waits for the recorded events and returns,
- * per kernel kind [0 kv_quant, 1 indexer scoring, 2 top-K select, 3 sparse attention], the
+ * per kernel kind [0 kv_quant (and the norm-rotate-write and read-back passes), 1 indexer
+ * scoring, 2 top-K select, 3 sparse attention (and the tree attention)], the
  * number of launches and their summed device time in milliseconds (host arrays of 4), then
  * clears the records. */
 fp4kv_status fp4kv_profile_enable(int32_t on);

@@ -1,0 +1,623 @@
+"""The operators that prepare and verify drafted tokens: qkv_norm_rope_fp4, kv_dequant_fp4 and
+tree_attn_decode against plain formulas in 64 bits, their refusals, and a run of them together.
+
+Tolerances:
+* the KV row's bf16 value, cache bytes and read-back values: exact;
+* queries: half a bf16 step of the value (2^-8 relative) and, before it, fp32 arithmetic: a sum of
+  squares of at most 1024 terms, at most 32 of them in sequence per lane and 5 joining steps, so
+  r is off by at most 20 x 2^-24 relative and a rotated channel by a few 2^-24 of |u_a| + |u_b|:
+  2^-18 (|u_a| + |u_b|) r covers both;
+* tree attention: half a bf16 step of the value; the probabilities are multiplied as fp16 (2^-11
+  relative each), and a logit is an fp32 sum of 512 products, whose order and rounding leave at
+  most 2^-16 of scale x sum |q v|. With A = sum_j p_j |v_j| an output is off by at most
+  2^-8 |o| + (2^-11 + 2 dz) A, lse by dz and its own fp32 rounding. No floating type holds every
+  probability to a relative 2^-11: fp16 has a step of 2^-24 below 2^-14, so a p that is stored as at
+  least 2^3 at the row's maximum is off by up to 2^-25 / 2^3 = 2^-28 of that maximum (<= 1), which
+  adds 2^-28 sum_j |v_j|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from fp4_sparse_attention_kv_b200 import binding
+from oracle import fp4kv_oracle as O
+from tests import parity as P
+
+DEV = "cuda"
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fk(cuda_lib):
+    import fp4_sparse_attention_kv_b200 as fk
+    return fk
+
+
+# ----------------------------------------------------------------------------------------
+# plain forms, 64 bits
+# ----------------------------------------------------------------------------------------
+
+def plain_norm_rope(x, w, pos, table, rope, half, eps):
+    """x bf16 [..., d] with one position per leading row -> (y, |u_a| + |u_b| (or |u|) times r), fp64."""
+    x = x.double()
+    d = x.shape[-1]
+    r = 1.0 / torch.sqrt((x * x).sum(-1, keepdim=True) / d + eps)
+    u = x * w.double() if w is not None else x.clone()
+    y, mag = u.clone(), u.abs()
+    if rope:
+        t = table.double()[pos]
+        c, s = t[:, : rope // 2], t[:, rope // 2:]
+        if x.dim() == 3:
+            c, s = c[:, None], s[:, None]
+        z = torch.arange(d - rope, d, device=x.device)
+        ia, ib = (z[: rope // 2], z[rope // 2:]) if half else (z[0::2], z[1::2])
+        a, b = u[..., ia], u[..., ib]
+        y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+        mag[..., ia] = mag[..., ib] = a.abs() + b.abs()
+    return y * r, mag * r
+
+
+def bf16_of_f64(y):
+    """fp64 -> bf16 bits, one rounding to nearest even (through an odd-rounded fp32)."""
+    f = y.float()
+    over = f.double().abs() > y.abs()
+    bits = f.view(torch.int32)
+    bits = torch.where(over, bits - 1, bits)  # towards zero
+    exact = bits.view(torch.float32).double() == y
+    bits = torch.where(exact, bits, bits | 1)
+    return bits.view(torch.float32).bfloat16()
+
+
+def cache_values(packed, scales):
+    return torch.from_numpy(O.kv_dequant_fp4(packed.cpu().numpy(), scales.cpu().numpy()))
+
+
+def plain_tree(q, packed, scales, lens, mask, drafts, idx, scale, b, t):
+    """One token's (out [H, 512], lse [H], bound on what out may be off before its rounding, dz [H]), fp64."""
+    cap = packed.shape[0]
+    n = max(0, min(int(lens[b]), cap))
+    pre = list(range(n)) if idx is None else [int(i) for i in idx[b].tolist() if 0 <= i < n]
+    m = int(mask[b, t])
+    rows = pre + [n + j for j in range(drafts[b]) if (m >> j) & 1 and n + j < cap]
+    H = q.shape[2]
+    if not rows:
+        z = torch.zeros(H, 512, dtype=torch.float64)
+        return z, torch.full((H,), -np.inf, dtype=torch.float64), z, torch.zeros(H, dtype=torch.float64)
+    r = torch.tensor(rows, device=packed.device)
+    v = cache_values(packed[r], scales[r])
+    qq = q[b, t].double().cpu()
+    z = qq @ v.T * scale
+    p = torch.softmax(z, -1)
+    dz = 2.0 ** -16 * abs(scale) * (qq.abs() @ v.abs().T).amax(-1)
+    return p @ v, torch.logsumexp(z, -1), p @ v.abs() * (2.0 ** -11 + 2 * dz[:, None]) + 2.0 ** -28 * v.abs().sum(0), dz
+
+
+def check_tree(fk, q, packed, scales, lens, mask, drafts, idx, scale, out, lse, what=""):
+    B, T = q.shape[:2]
+    for b in range(B):
+        for t in range(drafts[b]):
+            ro, rl, slack, dz = plain_tree(q, packed[b], scales[b], lens, mask, drafts, idx, scale, b, t)
+            o, l = out[b, t].double().cpu(), lse[b, t].double().cpu()
+            assert torch.isfinite(o).all(), f"{what} b={b} t={t}: out not finite"
+            tol = 2.0 ** -8 * ro.abs() + slack
+            bad = ((o - ro).abs() - tol).max()
+            assert bad <= 0, f"{what} b={b} t={t}: out off by {bad:.3e} above its tolerance"
+            inf = torch.isinf(rl)
+            assert torch.equal(torch.isneginf(l), inf), f"{what} b={b} t={t}: lse -inf"
+            if not inf.any():
+                assert ((l - rl).abs() <= dz + 2.0 ** -21 * rl.abs() + 2.0 ** -20).all(), f"{what} b={b} t={t}: lse"
+
+
+def table_of(top, rope, seed=0):
+    f = 10000.0 ** (-torch.arange(0, rope, 2, dtype=torch.float64) / max(rope, 1))
+    a = torch.arange(top, dtype=torch.float64)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float().to(DEV)
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def make_cache(fk, B, cap, seed, d=512):
+    x = torch.randn(B * cap, d, generator=gen(seed), device=DEV)
+    x[:, ::101] *= 20.0
+    packed = torch.empty(B, cap, d // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(B, cap, d // 16, dtype=torch.uint8, device=DEV)
+    fk.kv_quant_fp4(x.bfloat16(), packed.view(-1, d // 2), scales.view(-1, d // 16))
+    return packed, scales
+
+
+def tree_masks(B, T, seed):
+    """Random trees: every token sees itself and its ancestors."""
+    rng = np.random.default_rng(seed)
+    m = np.zeros((B, T), dtype=np.uint64)
+    for b in range(B):
+        for j in range(T):
+            par = int(rng.integers(-1, j)) if j else -1
+            m[b, j] = (m[b, par] if par >= 0 else np.uint64(0)) | np.uint64(1 << j)
+    return torch.from_numpy(m.view(np.int64)).to(DEV)
+
+
+# ----------------------------------------------------------------------------------------
+# refusals (CPU): the C entries check before the first CUDA call, the binding before that
+# ----------------------------------------------------------------------------------------
+
+def _c(name, *args):
+    L = binding.lib()
+    return getattr(L, name)(*args), L.fp4kv_last_error().decode()
+
+
+FAKE = 0x10000
+
+
+def _norm_args(**k):
+    a = dict(q=FAKE, qts=64 * 512, qhs=512, H=64, qw=None, qo=FAKE, kv=FAKE, kvs=512, kw=None, kvo=None, dst=None,
+             packed=FAKE, scales=FAKE, cap=16, n=4, d=512, rope=64, half=0, pos=FAKE, cs=FAKE, mp=10, eps=1e-6, st=None)
+    a.update(k)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("change, status, word", [
+    (dict(d=48), 2, "d=48"), (dict(d=1056, kvs=1056), 2, "d=1056"), (dict(rope=24), 2, "rope_dim=24"),
+    (dict(rope=528), 2, "rope_dim=528"), (dict(rope=-16), 2, "rope_dim"), (dict(eps=0.0), 1, "eps"),
+    (dict(eps=float("nan")), 1, "eps"), (dict(eps=float("inf")), 1, "eps"), (dict(q=None, kv=None), 1, "null q and kv"),
+    (dict(H=0), 2, "H=0"), (dict(H=129), 2, "H=129"), (dict(qo=None), 1, "q_out"), (dict(packed=None), 1, "neither"),
+    (dict(scales=None), 1, "scales"), (dict(pos=None), 1, "positions"), (dict(cs=None), 1, "cos_sin"),
+    (dict(qhs=504), 1, "strides"), (dict(qts=516), 1, "strides"), (dict(kvs=516), 1, "kv_row_stride"),
+    (dict(kvs=0), 1, "kv_row_stride"), (dict(q=FAKE + 8), 1, "aligned"), (dict(kv=FAKE + 2), 1, "aligned"),
+    (dict(cs=FAKE + 4), 1, "aligned"), (dict(packed=FAKE + 4), 1, "aligned"), (dict(n=17), 1, "cap_rows"),
+    (dict(n=-1), 1, "negative"), (dict(mp=-1), 1, "negative"), (dict(kv=None), 1, "packed needs kv"),
+])
+def test_norm_rope_refusals(change, status, word):
+    st, msg = _c("fp4kv_qkv_norm_rope_fp4", *_norm_args(**change))
+    assert st == status and word in msg, (st, msg)
+
+
+def test_no_rows_is_a_success_without_pointers():
+    st, msg = _c("fp4kv_qkv_norm_rope_fp4", *_norm_args(n=0, qo=None, packed=None, scales=None, pos=None, cs=None))
+    assert (st, msg) == (0, "")
+    assert _c("fp4kv_kv_dequant_fp4", None, None, 0, 512, None, 0, None, 0, 512, None) == (0, "")
+
+
+@pytest.mark.parametrize("change, status, word", [
+    (dict(d=40), 2, "d=40"), (dict(packed=None), 1, "null"), (dict(scales=None), 1, "null"), (dict(out=None), 1, "null"),
+    (dict(stride=504), 1, "stride"), (dict(stride=516), 1, "stride"), (dict(out=FAKE + 8), 1, "aligned"),
+    (dict(packed=FAKE + 8), 1, "aligned"), (dict(n=11), 1, "cap_rows"), (dict(n=-1), 1, "negative"),
+    (dict(cap=-1), 1, "negative"),
+])
+def test_dequant_refusals(change, status, word):
+    a = dict(packed=FAKE, scales=FAKE, cap=10, d=512, src=None, n=4, out=FAKE, f32=0, stride=512, st=None)
+    a.update(change)
+    st, msg = _c("fp4kv_kv_dequant_fp4", *a.values())
+    assert st == status and word in msg, (st, msg)
+
+
+@pytest.mark.parametrize("change, status, word", [
+    (dict(B=0), 2, "B=0"), (dict(B=65536), 2, "B=65536"), (dict(T=0), 2, "T=0"), (dict(T=65), 2, "T=65"),
+    (dict(H=0), 2, "H=0"), (dict(H=129), 2, "H=129"), (dict(d=256), 2, "d=256"), (dict(top_k=0), 2, "top_k=0"),
+    (dict(top_k=(1 << 20) + 1), 2, "top_k"), (dict(idx=None), 2, "top_k"), (dict(cap=0), 2, "cap=0"),
+    (dict(cap=1 << 31), 2, "cap"), (dict(q=None), 1, "null"), (dict(mask=None), 1, "null"), (dict(ws=None), 1, "null"),
+    (dict(out=FAKE + 8), 1, "misaligned"), (dict(ws=FAKE + 16), 1, "misaligned"), (dict(mask=FAKE + 4), 1, "misaligned"),
+    (dict(wsb=255), 4, "ws_bytes"),
+])
+def test_tree_refusals(change, status, word):
+    a = dict(q=FAKE, B=2, T=5, H=64, d=512, packed=FAKE, scales=FAKE, cap=100, lens=FAKE, nd=None, mask=FAKE, idx=FAKE,
+             top_k=16, scale=1.0, out=FAKE, lse=None, ws=FAKE, wsb=1 << 30, st=None)
+    a.update(change)
+    a["scale"] = ctypes.c_float(a["scale"])
+    st, msg = _c("fp4kv_tree_attn_decode", *a.values())
+    assert st == status and word in msg, (st, msg)
+
+
+def test_tree_workspace_sizes():
+    wb = binding.workspace_bytes
+    assert wb(binding.OP_TREE_ATTN, 4, 32784, 16 * 64, 0) >= 256
+    assert wb(binding.OP_TREE_ATTN, 4, 32784, 0, 0) == 0
+    # the smaller problem never needs more
+    assert wb(binding.OP_TREE_ATTN, 1, 100, 8, 0) <= wb(binding.OP_TREE_ATTN, 1, 100000, 8 * 64, 0)
+
+
+def test_binding_refuses_cpu_tensors_and_missing_arguments():
+    x = torch.zeros(2, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.qkv_norm_rope_fp4(None, None)
+    with pytest.raises(TypeError):
+        binding.qkv_norm_rope_fp4(None, x)
+    with pytest.raises(TypeError):
+        binding.kv_dequant_fp4(torch.zeros(2, 256, dtype=torch.uint8), torch.zeros(2, 32, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        binding.tree_attn_decode(torch.zeros(1, 1, 1, 512, dtype=torch.bfloat16), None, None, None, None)
+
+
+# ----------------------------------------------------------------------------------------
+# kv_dequant_fp4
+# ----------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dequant_every_code_and_scale(fk, dtype):
+    """All 256 code bytes under all 254 finite scale bytes."""
+    sc = torch.tensor([s for s in range(256) if s & 0x7f != 0x7f], dtype=torch.uint8)
+    packed = torch.arange(256, dtype=torch.uint8).view(1, 256).repeat(len(sc), 1).to(DEV)
+    scales = sc[:, None].repeat(1, 32).to(DEV)
+    got = fk.kv_dequant_fp4(packed, scales, dtype=dtype)
+    want = cache_values(packed, scales)
+    assert torch.equal(got.double().cpu(), want)
+    assert torch.equal(torch.signbit(got.cpu()), torch.signbit(want))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d, cap, n", [(32, 5, 3), (64, 1, 1), (96, 700, 1001), (128, 33, 4000), (512, 1000, 257),
+                                       (512, 3000, 60001), (576, 64, 129), (1024, 100, 3001)])
+def test_dequant_gather(fk, d, cap, n, dtype):
+    packed, scales = make_cache(fk, 1, cap, d + n, d)
+    packed, scales = packed[0], scales[0]
+    src = torch.randint(0, cap, (n,), generator=gen(n), device=DEV)
+    src[::7] = torch.tensor([-1, cap, 1 << 40, -(1 << 40)], device=DEV).repeat(n)[: len(src[::7])]
+    wide = torch.full((n, d + 8), 7.0, dtype=dtype, device=DEV)  # a row stride above d
+    got = fk.kv_dequant_fp4(packed, scales, src_row=src, out=wide[:, :d])
+    ok = (src >= 0) & (src < cap)
+    want = cache_values(packed, scales).to(DEV)[src.clamp(0, cap - 1)] * ok[:, None]
+    assert torch.equal(got.double(), want)
+    assert (wide[:, d:] == 7.0).all()
+    assert torch.equal(fk.kv_dequant_fp4(packed, scales, dtype=dtype).double().cpu(), cache_values(packed, scales))
+
+
+@gpu
+def test_dequant_inverts_the_quantizer_and_takes_no_rows(fk):
+    packed, scales = make_cache(fk, 2, 40, 3)
+    x = fk.kv_dequant_fp4(packed, scales)
+    p2, s2 = torch.empty_like(packed), torch.empty_like(scales)
+    fk.kv_quant_fp4(x, p2.view(-1, 256), s2.view(-1, 32))
+    assert torch.equal(fk.kv_dequant_fp4(p2, s2), x)  # every group has a code 6, so its scale comes back too
+    none = fk.kv_dequant_fp4(packed, scales, src_row=torch.empty(0, dtype=torch.int64, device=DEV))
+    assert none.shape == (0, 512)
+    with pytest.raises(ValueError):
+        fk.kv_dequant_fp4(packed, scales, out=torch.empty(79, 512, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(TypeError):
+        fk.kv_dequant_fp4(packed, scales, out=torch.empty(80, 512, dtype=torch.float16, device=DEV))
+
+
+# ----------------------------------------------------------------------------------------
+# qkv_norm_rope_fp4
+# ----------------------------------------------------------------------------------------
+
+def norm_inputs(n, H, d, seed, loud=True):
+    g = gen(seed)
+    q = (torch.randn(n, max(H, 1), d, generator=g, device=DEV) * 3).bfloat16() if H else None
+    kv = torch.randn(n, d, generator=g, device=DEV)
+    if loud and n:
+        kv[:, 3] *= 50.0
+        kv[0] = 0.0  # a row of zeros
+        kv[-1] *= 1e-3
+    qw = (1 + 0.2 * torch.randn(d, generator=g, device=DEV)).bfloat16()
+    kw = (1 + 0.2 * torch.randn(d, generator=g, device=DEV)).bfloat16()
+    return q, kv.bfloat16(), qw, kw
+
+
+def check_q(got, q, w, pos, table, rope, half, eps):
+    y, mag = plain_norm_rope(q, w, pos, table, rope, half, eps)
+    tol = 2.0 ** -8 * y.abs() + 2.0 ** -18 * mag
+    assert ((got.double() - y).abs() <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("weight", [True, False])
+@pytest.mark.parametrize("n, H, d, rope, half", [
+    (1, 64, 512, 64, False), (1, 1, 32, 0, False), (3, 1, 32, 32, True), (130, 5, 64, 64, False), (777, 32, 128, 64, True),
+    (33, 12, 96, 48, False), (33, 12, 96, 96, True), (50, 8, 192, 128, True), (64, 3, 256, 16, False),
+    (64, 128, 320, 0, False), (500, 2, 512, 512, True), (129, 16, 576, 64, False), (17, 7, 1024, 128, True),
+    (5000, 0, 512, 64, True), (5000, 0, 512, 64, False)])
+def test_norm_rope(fk, n, H, d, rope, half, weight):
+    q, kv, qw, kw = norm_inputs(n, H, d, n + d)
+    qw, kw = (qw, kw) if weight else (None, None)
+    top = 4096
+    table = table_of(top, rope)
+    pos = torch.randint(0, top, (n,), generator=gen(n), device=DEV)
+    cap = n + 9
+    dst = torch.randperm(cap, generator=gen(d), device=DEV)[:n]
+    skip = torch.arange(n, device=DEV) % 11 == 5
+    dst = torch.where(skip, torch.where(torch.arange(n, device=DEV) % 2 == 0, -1, cap), dst)
+    packed = torch.full((cap, d // 2), 0xAB, dtype=torch.uint8, device=DEV)
+    scales = torch.full((cap, d // 16), 0xCD, dtype=torch.uint8, device=DEV)
+    kv_out = torch.full((n, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    for eps in (1e-6, 1e-2):
+        qo, ko = fk.qkv_norm_rope_fp4(q, kv, positions=pos, cos_sin=table, rope_dim=rope, rope_half=half, q_weight=qw,
+                                      kv_weight=kw, eps=eps, packed=packed, scales=scales, dst_row=dst, kv_out=kv_out)
+        if H:
+            check_q(qo, q, qw, pos, table, rope, half, eps)
+        want = bf16_of_f64(plain_norm_rope(kv, kw, pos, table, rope, half, eps)[0])
+        assert torch.equal(ko, want)
+        op, os_ = O.kv_quant_fp4(P.to_f64(want))
+        live = (dst >= 0) & (dst < cap)
+        assert torch.equal(packed[dst[live]].cpu(), torch.from_numpy(op)[live.cpu()])
+        assert torch.equal(scales[dst[live]].cpu(), torch.from_numpy(os_)[live.cpu()])
+        rest = torch.ones(cap, dtype=torch.bool, device=DEV)
+        rest[dst[live]] = False
+        assert (packed[rest] == 0xAB).all() and (scales[rest] == 0xCD).all()
+
+
+@gpu
+def test_norm_rope_strides_in_place_and_tokens_left_alone(fk):
+    n, H, d, rope = 40, 6, 128, 64
+    g = gen(5)
+    fused = torch.randn(n, (H + 2) * d, generator=g, device=DEV).bfloat16()  # one projection's output
+    q, kv = fused[:, : H * d].view(n, H, d), fused[:, H * d: (H + 1) * d]
+    table, pos = table_of(100, rope), torch.randint(0, 100, (n,), generator=g, device=DEV)
+    pos[3], pos[17] = -1, 100  # outside the table: these tokens are left alone
+    gone = (pos < 0) | (pos >= 100)
+    kw = dict(positions=pos, cos_sin=table, rope_dim=rope, rope_half=True)
+    qo = torch.full((n, H, d), 9.0, dtype=torch.bfloat16, device=DEV)
+    ko = torch.full((n, d), 9.0, dtype=torch.bfloat16, device=DEV)
+    fk.qkv_norm_rope_fp4(q, kv, q_out=qo, kv_out=ko, **kw)
+    assert (qo[gone] == 9.0).all() and (ko[gone] == 9.0).all()
+    keep = ~gone
+    check_q(qo[keep], q[keep], None, pos[keep], table, rope, True, 1e-6)
+    # heads outermost, and an output over its own input
+    qt = q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert qt.stride() != q.contiguous().stride()
+    assert torch.equal(fk.qkv_norm_rope_fp4(qt, None, **kw)[0][keep], qo[keep])
+    qi, ki = q.contiguous(), kv.contiguous()
+    fk.qkv_norm_rope_fp4(qi, ki, q_out=qi, kv_out=ki, **kw)
+    assert torch.equal(qi[keep], qo[keep]) and torch.equal(ki[keep], ko[keep])
+    assert torch.equal(qi[gone], q[gone])
+    # the KV row alone, queries alone, nothing at all
+    assert torch.equal(fk.qkv_norm_rope_fp4(None, kv, **kw)[1][keep], ko[keep])
+    none = fk.qkv_norm_rope_fp4(q[:0], kv[:0], positions=pos[:0], cos_sin=table, rope_dim=rope)
+    assert none[0].shape == (0, H, d) and none[1].shape == (0, d)
+    with pytest.raises(ValueError):
+        fk.qkv_norm_rope_fp4(q, kv, rope_dim=32, positions=pos, cos_sin=table)
+    with pytest.raises(ValueError):
+        fk.qkv_norm_rope_fp4(q, kv[:5], **kw)
+    with pytest.raises(ValueError):
+        fk.qkv_norm_rope_fp4(q, None, packed=torch.empty(n, 64, dtype=torch.uint8, device=DEV), **kw)
+
+
+# ----------------------------------------------------------------------------------------
+# tree_attn_decode
+# ----------------------------------------------------------------------------------------
+
+def run_tree(fk, B, T, H, lens, drafts, cap, idx=None, seed=0, scale=512 ** -0.5, q=None, mask=None, cache=None, ws=None):
+    packed, scales = make_cache(fk, B, cap, seed) if cache is None else cache
+    if q is None:
+        q = torch.randn(B, T, H, 512, generator=gen(seed + 1), device=DEV).bfloat16()
+    if mask is None:
+        mask = tree_masks(B, T, seed)
+    out = torch.full((B, T, H, 512), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((B, T, H), 5.0, device=DEV)
+    lt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    nd = None if drafts is None else torch.tensor(drafts, dtype=torch.int32, device=DEV)
+    ret = fk.tree_attn_decode(q, packed, scales, lt, mask, n_draft=nd, idx=idx, sm_scale=scale, out=out, lse=lse, ws=ws)
+    assert ret[0] is out and ret[1] is lse
+    dr = [T] * B if drafts is None else [max(0, min(x, T)) for x in drafts]
+    check_tree(fk, q, packed, scales, lens, mask, dr, idx, scale, out, lse, f"B{B} T{T} H{H}")
+    for b in range(B):  # tokens behind the last draft keep what was there
+        assert (out[b, dr[b]:] == 3.0).all() and (lse[b, dr[b]:] == 5.0).all()
+    return q, packed, scales, lt, mask, nd, out, lse
+
+
+@gpu
+@pytest.mark.parametrize("B, T, H, lens, drafts, cap", [
+    (1, 1, 1, [0], None, 1),                       # the token alone
+    (1, 1, 64, [1], None, 2),
+    (1, 8, 64, [500], None, 508),
+    (2, 3, 20, [63, 64], None, 80),                # a prefix that ends at, and one row before, a tile's end
+    (3, 5, 12, [65, 127, 129], [5, 0, 2], 140),    # a sequence without drafts
+    (2, 64, 8, [130, 0], [64, 63], 300),           # 64 drafts, one sequence without a prefix
+    (1, 64, 128, [70], None, 134),                 # 8192 query rows
+    (4, 7, 64, [1000, 3, 777, 64], [7, 7, 99, -5], 1007),  # draft counts outside [0, T]
+    (1, 2, 6, [20000], None, 20002),               # few rows, a long prefix
+    (1, 16, 64, [4093], None, 4100),               # the cache ends inside the drafts
+    (2, 4, 16, [50, 9999], None, 60),              # a length behind the cache's end
+    (33, 2, 3, [(i * 37) % 200 for i in range(33)], None, 202),
+])
+def test_tree_dense(fk, B, T, H, lens, drafts, cap):
+    run_tree(fk, B, T, H, lens, drafts, cap, seed=B + T + H)
+
+
+@gpu
+@pytest.mark.parametrize("B, T, H, lens, cap, K", [
+    (1, 1, 64, [300], 310, 1), (3, 5, 64, [3000, 0, 40], 3005, 512), (2, 8, 20, [5000, 4999], 5008, 2048),
+    (2, 33, 7, [100, 90], 140, 65), (1, 4, 16, [6000], 6004, 5000)])
+def test_tree_selected(fk, B, T, H, lens, cap, K):
+    idx = torch.full((B, K), -1, dtype=torch.int32, device=DEV)
+    for b in range(B):
+        k = min(K, lens[b])
+        idx[b, :k] = torch.randperm(max(lens[b], 1), generator=gen(b), device=DEV)[:k].sort().values.int()
+    run_tree(fk, B, T, H, lens, None, cap, idx=idx, seed=K)
+
+
+@gpu
+def test_tree_selection_in_any_order_with_holes_and_repeats(fk):
+    B, T, H, cap, K = 2, 6, 24, 400, 200
+    idx = torch.randint(0, 390, (B, K), generator=gen(1), device=DEV).int()
+    idx[:, ::5] = -1
+    idx[0, 1], idx[0, 2], idx[1, 3] = 2 ** 31 - 1, -2 ** 31, 391  # absent all the same
+    idx[1, 64:128] = -1  # a whole tile absent
+    idx[0, 10:20] = 7  # one row ten times
+    run_tree(fk, B, T, H, [390, 390], [6, 4], cap, idx=idx, seed=9)
+
+
+@gpu
+def test_tree_masks_of_every_kind(fk):
+    """Empty masks over an empty prefix (out 0, lse -inf), a token blind to itself, bits behind the
+    last draft, the highest bit."""
+    B, T, H = 2, 64, 5
+    mask = tree_masks(B, T, 4)
+    mask[:, 0] = 0
+    mask[:, 1] = -1            # every bit
+    mask[:, 2] = 1 << 1        # another draft only
+    mask[:, 3] = -(1 << 63)    # the last draft only
+    q, packed, scales, lt, mask, nd, out, lse = run_tree(fk, B, T, H, [0, 90], [64, 40], 160, mask=mask, seed=2)
+    assert (out[0, 0] == 0).all() and torch.isneginf(lse[0, 0]).all()
+
+
+@gpu
+def test_tree_rows_nobody_sees_may_hold_anything(fk):
+    """Drafted rows outside every mask, rows of the prefix outside the selection and rows behind the
+    last draft hold bytes that stand for NaN."""
+    B, T, H, cap = 2, 5, 64, 300
+    packed, scales = make_cache(fk, B, cap, 6)
+    lens, drafts = [200, 131], [5, 3]
+    mask = torch.zeros(B, T, dtype=torch.int64, device=DEV)
+    mask[:] = 0b00101  # drafts 1, 3, 4 are seen by nobody
+    idx = torch.arange(0, 120, 2, dtype=torch.int32, device=DEV).repeat(B, 1)
+    for b in range(B):
+        keep = torch.zeros(cap, dtype=torch.bool, device=DEV)
+        keep[idx[b].long()] = True
+        keep[lens[b]], keep[lens[b] + 2] = True, True
+        scales[b][~keep] = 0x7F
+    run_tree(fk, B, T, H, lens, drafts, cap, idx=idx, mask=mask, cache=(packed, scales), seed=7)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1.0, 0.3, -0.05, 0.0])
+def test_tree_large_logits_that_grow_along_the_prefix(fk, scale):
+    """Logits up to a few thousand whose running maximum keeps moving, in every tile and head at
+    another place."""
+    B, T, H, n = 1, 3, 50, 1500
+    g = gen(11)
+    x = torch.randn(n + T, 512, generator=g, device=DEV)
+    x *= torch.linspace(0.01, 4.0, n + T, device=DEV)[:, None]
+    packed = torch.empty(1, n + T, 256, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(1, n + T, 32, dtype=torch.uint8, device=DEV)
+    fk.kv_quant_fp4(x.bfloat16(), packed[0], scales[0])
+    q = torch.randn(B, T, H, 512, generator=g, device=DEV) * torch.logspace(-3, 1, H, device=DEV)[:, None]
+    run_tree(fk, B, T, H, [n], None, n + T, cache=(packed, scales), q=q.bfloat16(), scale=scale, seed=1)
+
+
+@gpu
+def test_tree_extreme_queries(fk):
+    """Zero queries (a plain mean), one loud channel, queries near bf16's ends."""
+    B, T, H, n = 1, 2, 8, 700
+    q = torch.randn(B, T, H, 512, generator=gen(3), device=DEV)
+    q[0, 0, 0] = 0.0
+    q[0, 0, 1, 1:] = 0.0
+    q[0, 0, 2] *= 1e-30
+    q[0, 0, 3, 7] = 300.0
+    run_tree(fk, B, T, H, [n], None, n + T, q=q.bfloat16(), scale=0.02, seed=3)
+    run_tree(fk, B, T, H, [n], None, n + T, q=(q * 1e30).bfloat16(), scale=2e-32, seed=3)
+
+
+@gpu
+def test_tree_binding_checks(fk):
+    q, packed, scales, lt, mask, nd, out, lse = run_tree(fk, 1, 2, 4, [10], None, 12)
+    o, l = fk.tree_attn_decode(q, packed, scales, lt, mask, sm_scale=512 ** -0.5)
+    assert torch.equal(o, out) and torch.equal(l, lse)
+    assert fk.tree_attn_decode(q, packed, scales, lt, mask, want_lse=False)[1] is None
+    with pytest.raises(ValueError):
+        fk.tree_attn_decode(q[0], packed, scales, lt, mask)
+    with pytest.raises(ValueError):
+        fk.tree_attn_decode(q, packed[:, :, :128], scales, lt, mask)
+    with pytest.raises(ValueError):
+        fk.tree_attn_decode(q, packed, scales, lt, mask[:, :1])
+    with pytest.raises(TypeError):
+        fk.tree_attn_decode(q, packed, scales, lt.long(), mask)
+    with pytest.raises(ValueError):
+        fk.tree_attn_decode(q, packed, scales, lt, mask, out=out[:, :1])
+    with pytest.raises(fk.Fp4kvError):
+        fk.tree_attn_decode(q, packed, scales, lt, mask, ws=torch.zeros(128, dtype=torch.uint8, device=DEV))
+
+
+@gpu
+def test_tree_same_bits_every_time_and_from_a_replayed_graph(fk):
+    """Nothing depends on timing; graphs that share a workspace replay one after another; lengths
+    are read at replay."""
+    B, T, H, cap = 3, 6, 64, 5000
+    ws = fk.alloc_workspace(fk.workspace_bytes(fk.OP_TREE_ATTN, B, cap, T * H, 0), DEV)
+    q, packed, scales, lt, mask, nd, out, lse = run_tree(fk, B, T, H, [4990, 17, 2222], [6, 6, 4], cap, seed=5, ws=ws)
+    ref = out.clone(), lse.clone()
+    for _ in range(3):
+        fk.tree_attn_decode(q, packed, scales, lt, mask, n_draft=nd, sm_scale=512 ** -0.5, ws=ws, out=out, lse=lse)
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for i in range(2):
+        o, l = torch.full_like(out, 3.0), torch.full_like(lse, 5.0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fk.tree_attn_decode(q, packed, scales, lt, mask, n_draft=nd, sm_scale=512 ** -0.5, ws=ws, out=o, lse=l)
+        graphs.append(g)
+        outs.append((o, l))
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, l in outs:
+        assert torch.equal(o, ref[0]) and torch.equal(l, ref[1])
+    lt.copy_(torch.tensor([100, 3000, 0], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    check_tree(fk, q, packed, scales, lt.tolist(), mask, [6, 6, 4], None, 512 ** -0.5, *outs[0])
+    assert fk.workspace_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------------------
+# together
+# ----------------------------------------------------------------------------------------
+
+@gpu
+def test_a_step_of_verifying_drafts(fk):
+    """Norm, rotation and write of the drafts' rows behind the prefix, attention of the tree, the
+    accepted row read back; the same tokens decoded one by one with sparse_attn_decode agree."""
+    B, T, H, d, rope, n = 3, 4, 64, 512, 64, 600
+    cap = n + T
+    packed, scales = make_cache(fk, B, cap, 21)
+    lens = [n, 333, 64]
+    g = gen(22)
+    qkv = torch.randn(B * T, (H + 1) * d, generator=g, device=DEV).bfloat16()
+    w = (1 + 0.1 * torch.randn(d, generator=g, device=DEV)).bfloat16()
+    table = table_of(cap, rope)
+    lt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    pos = (lt.long()[:, None] + torch.arange(T, device=DEV)).view(-1)
+    dst = pos + torch.arange(B, device=DEV).repeat_interleave(T) * cap
+    q, _ = fk.qkv_norm_rope_fp4(qkv[:, : H * d].view(B * T, H, d), qkv[:, H * d:], positions=pos, cos_sin=table,
+                                rope_dim=rope, q_weight=w, kv_weight=w, packed=packed, scales=scales, dst_row=dst)
+    chain = torch.tensor([[(1 << (t + 1)) - 1 for t in range(T)]] * B, dtype=torch.int64, device=DEV)
+    scale = d ** -0.5
+    out, lse = fk.tree_attn_decode(q.view(B, T, H, d), packed, scales, lt, chain, sm_scale=scale)
+    rows = fk.kv_dequant_fp4(packed, scales, src_row=dst)
+    check_tree(fk, q.view(B, T, H, d), packed, scales, lens, chain, [T] * B, None, scale, out, lse)
+    y = plain_norm_rope(qkv[:, H * d:], w, pos, table, rope, False, 1e-6)[0]
+    op, os_ = O.kv_quant_fp4(P.to_f64(bf16_of_f64(y)))
+    assert np.array_equal(rows.double().cpu().numpy(), O.kv_dequant_fp4(op, os_))
+    idx = torch.arange(cap, dtype=torch.int32, device=DEV).repeat(B, 1)
+    for t in range(T):
+        one, l1 = fk.sparse_attn_decode(q.view(B, T, H, d)[:, t].contiguous(), packed, scales, lt + t + 1, idx, scale)
+        assert (l1 - lse[:, t]).abs().max() <= 1e-4
+        assert (one - out[:, t].float()).abs().max() <= 5e-3 + 2.0 ** -8 * one.abs().max()
+
+
+@gpu
+def test_norm_output_feeds_the_attention_at_once(fk):
+    """No synchronisation between the kernel that makes q (and the cache row) and those that read
+    them, many times over, also on a side stream."""
+    n, H, d = 600, 64, 512
+    packed, scales = make_cache(fk, 1, n, 31)
+    idx = torch.arange(256, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    ws = fk.alloc_workspace(fk.workspace_bytes(fk.OP_SPARSE_ATTN, 1, n, H, 256), DEV)
+    raw = [torch.randn(1, H, d, generator=gen(40 + i), device=DEV).bfloat16() for i in range(8)]
+    q = torch.empty(1, H, d, dtype=torch.bfloat16, device=DEV)
+    outs = [torch.empty(1, H, d, device=DEV) for _ in raw]
+    want = []
+    for x in raw:
+        y, _ = fk.qkv_norm_rope_fp4(x, None)
+        torch.cuda.synchronize()
+        want.append(fk.sparse_attn_decode(y, packed, scales, lens, idx, 0.04, ws=ws, want_lse=False)[0].clone())
+        torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                for x, o in zip(raw, outs):
+                    fk.qkv_norm_rope_fp4(x, None, q_out=q)
+                    fk.sparse_attn_decode(q, packed, scales, lens, idx, 0.04, ws=ws, out=o, want_lse=False)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
