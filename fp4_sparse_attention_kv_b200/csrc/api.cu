@@ -169,13 +169,24 @@ AttnLayout attn_layout(int64_t B, int64_t H, int64_t top_k, int sms) {
 }
 
 struct TreeLayout {
-  size_t total = kAlign;  // status word
+  size_t first_tile = 0, part_ml = 0, part_o = 0, total = 0;
+  int n_clusters = 1;
 };
 
-// rows: T * H query rows per sequence; top_k 0: every row of the prefix is attended
+// rows: T * H query rows per sequence; top_k 0: every row of the prefix is attended. A cluster
+// leaves at most two unfinished items: the one it begins with and the one it ends with.
 TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int sms) {
-  (void)B, (void)rows, (void)cap, (void)top_k, (void)sms;
-  return TreeLayout{};
+  TreeLayout L;
+  L.n_clusters = fp4kv::tree_clusters(B, rows, cap, top_k, sms);
+  size_t off = kAlign;  // status header
+  L.first_tile = off;
+  off += up(sizeof(int64_t) * (B + 1));
+  L.part_ml = off;
+  off += up(sizeof(float) * 2 * L.n_clusters * 128 * 2);
+  L.part_o = off;
+  off += up(sizeof(float) * 2 * L.n_clusters * 128 * 512);
+  L.total = off;
+  return L;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -715,11 +726,17 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
   p.sm_scale = sm_scale;
   p.out = out;
   p.lse = lse;
-  p.status = static_cast<uint32_t*>(ws);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  p.n_clusters = L.n_clusters;
+  p.min_tiles = fp4kv::tree_min_tiles();
+  p.first_tile = reinterpret_cast<int64_t*>(base + L.first_tile);
+  p.part_ml = reinterpret_cast<float*>(base + L.part_ml);
+  p.part_o = reinterpret_cast<float*>(base + L.part_o);
+  p.status = reinterpret_cast<uint32_t*>(base);
   cudaError_t e;
   {
     prof::Scope ps(3, static_cast<cudaStream_t>(stream));
-    e = fp4kv::launch_tree_attn(p, sms, static_cast<cudaStream_t>(stream));
+    e = fp4kv::launch_tree_attn(p, static_cast<cudaStream_t>(stream));
   }
   if (e != cudaSuccess) return cuda_fail(e, "tree_attn_decode");
   return ok();

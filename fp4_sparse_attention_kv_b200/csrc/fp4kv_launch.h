@@ -145,9 +145,16 @@ struct TreeAttnParams {
   float sm_scale;
   uint16_t* out;              // [B][T][H][512] bf16
   float* lse;                 // nullable [B][T][H]
+  int n_clusters, min_tiles;  // tree_clusters(), tree_min_tiles()
+  int64_t* first_tile;        // workspace [B + 1]: each sequence's first tile, the number of tiles
+  float* part_ml;             // workspace [2 n_clusters][128][2]: reference and sum of unfinished items
+  float* part_o;              // workspace [2 n_clusters][128][512]
   uint32_t* status;
 };
-cudaError_t launch_tree_attn(const TreeAttnParams& p, int num_sms, cudaStream_t stream);
+// Clusters of two CTAs for sequences of `rows` = T * H query rows (the fewest tiles that one gets).
+int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms);
+int tree_min_tiles();
+cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------------------
 // Context-sharded decode: exact merge of per-range top-K candidates, and the log-sum-exp

@@ -8,12 +8,12 @@
 //
 // Numerics:
 //  * queries: fp32, rounded once to bf16. u = x w is exact in fp32 (two 8-bit significands).
-//  * the KV row: y is rounded to bf16 and that value is quantised, so the cache holds exactly what
-//    kv_quant_fp4 makes of kv_out. A code is decided by which side of a border a value falls on, so
-//    the rounding to bf16 is that of y itself, not of an fp32 approximation: sum x^2 and r are held
-//    in fp64, and y is formed in fp64 where its fp32 form lies within 3 units in the last place of a
-//    bf16 rounding border (fp32: r rounded, 2^-24, and one product, 2^-24: at most 2 units), and
-//    for the rotated channels, whose difference can cancel.
+//  * the KV row: y's nearest fp32 value is rounded to bf16 and that is quantised, so the cache holds
+//    exactly what kv_quant_fp4 makes of kv_out. A code is decided by which side of a border a value
+//    falls on, so y must not be off by even an fp32 step: sum x^2 and r are held in fp64, and y is
+//    formed in fp64 where a quick fp32 form of it lies within 3 units in the last place of a bf16
+//    rounding border (r rounded, 2^-24, and one product, 2^-24: at most 2 units), and for the
+//    rotated channels, whose difference can cancel.
 // Memory: LPR lanes share a row, each with GPL groups of 16 channels (two 16-byte loads a group).
 #include "fp4kv_common.cuh"
 #include "fp4kv_launch.h"
@@ -30,14 +30,8 @@ FP4KV_DEV uint32_t f32_to_bf16(float f) {  // round to nearest even
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
   return r;
 }
-// fp64 -> bf16, one rounding: to fp32 towards zero with the lost bits kept as a sticky last bit,
-// then to nearest even.
-FP4KV_DEV uint32_t f64_to_bf16(double y) {
-  const float f = __double2float_rz(y);
-  uint32_t u = __float_as_uint(f);
-  if (static_cast<double>(f) != y) u |= 1u;
-  return f32_to_bf16(__uint_as_float(u));
-}
+// (fp64 to fp32 to bf16, each to nearest even)
+FP4KV_DEV uint32_t f64_to_bf16(double y) { return f32_to_bf16(__double2float_rn(y)); }
 FP4KV_DEV float half_of(uint32_t w, int k) {  // channel k (0 low, 1 high) of a bf16 pair
   return __uint_as_float(k ? (w & 0xffff0000u) : (w << 16));
 }
