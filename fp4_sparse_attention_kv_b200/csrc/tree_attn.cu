@@ -20,10 +20,13 @@
 // A CTA (17 warps):
 //  * warps 8-15 dequantize: a tile's 64 half rows to fp16 (exact) in 128-byte-swizzled 64-channel
 //    chunks, K-major B operand of S and MN-major B operand of O; four stages, loads two tiles ahead;
-//  * warp 16 issues S(t + 1) (A = Q in TMEM), then O += P(t) V(t) (A = P in shared memory);
+//  * warp 16 issues S(t + 2) (A = Q in TMEM), then O += P(t) V(t) (A = P in shared memory);
 //  * warps 0-7 own TMEM lane quarter w % 4 (query rows) and column half w / 4. Those of the CTA's
 //    own rows add the two parts of S, keep reference and sum in registers (lane = query row), and
 //    write P; the others send their part of S over and take P's arrival.
+// What crosses over goes by bulk copies that complete on the receiver's barrier: 4 KiB of S per warp
+// and tile, 2 KiB of P. (Stores to the other CTA's memory, followed by a releasing arrival, held up the
+// SM's other shared-memory instructions: 6,300 cycles a tile. The link moves 20 bytes a cycle each way.)
 // Numerics: q as fp16 times a power of two per row (exact within 2^29 of the row's maximum), v exact
 // in fp16, S and O in fp32. The reference m moves only when a logit passes it by 2^9 (log2 domain),
 // to 2^3 above the maximum; p is stored as p * 2^6 in fp16, so the row's largest is at least 2^3 and at
@@ -48,28 +51,31 @@ constexpr float kMoveLog2 = 9.0f, kHeadroomLog2 = 3.0f, kPLog2 = 6.0f;
 
 constexpr uint32_t kVBytes = kTile * kHalf * 2;   // 32 KiB: 4 chunks of [64 rows][128 B]
 constexpr uint32_t kVChunk = kTile * 128;
-constexpr uint32_t kPBytes = kRows * 128;         // [128 query rows][64 cache rows] fp16
-constexpr uint32_t kSxBytes = 64 * kTile * 4;     // [16 column fours][64 query rows][4] fp32
+constexpr uint32_t kPBytes = kRows * 128;         // [2 halves of 32 cache rows][128 query rows][64 B] fp16
+constexpr uint32_t kSxBytes = 64 * kTile * 4;     // [4 warps][8 column fours][32 query rows][4] fp32
 constexpr uint32_t kOffV = 0;
 constexpr uint32_t kOffP = kOffV + kStages * kVBytes;
 constexpr uint32_t kOffSx = kOffP + 2 * kPBytes;
+constexpr uint32_t kOffSt = kOffSx + 2 * kSxBytes;  // S on its way out, [2 tiles], 4 KiB per warp
 constexpr uint32_t kOffQ = kOffP;                 // Q's way into TMEM: [128 rows][512 B] over P and Sx
 static_assert(2 * kPBytes + 2 * kSxBytes == kRows * kHalf * 2, "Q staging");
-constexpr uint32_t kOffBar = kOffSx + 2 * kSxBytes;
+constexpr uint32_t kOffBar = kOffSt + 2 * kSxBytes;
+constexpr uint32_t kOffMisc = kOffBar + 192;
 constexpr uint32_t kOffC = kOffBar + 256;         // [128] logit scale (log2 domain) per query row
 constexpr uint32_t kOffAx = kOffC + 512;          // [2][64] rescale factors of the other CTA's rows
 constexpr uint32_t kOffM = kOffAx + 512;          // [128] reference at the end
 constexpr uint32_t kOffL = kOffM + 512;           // [128] sum at the end
-constexpr uint32_t kOffPair = kOffL + 512;        // [2][2][64] exchange between a row's two threads: maxima, sums
-constexpr uint32_t kOffMisc = kOffPair + 1024;
-constexpr uint32_t kSmem = kOffMisc + 64;
+constexpr uint32_t kOffPair = kOffL + 512;        // [3][64] exchange between a row's two threads: maxima, one sum
+constexpr uint32_t kSmem = kOffPair + 768;
 static_assert(kSmem <= 232448, "shared memory");
 
 // TMEM columns: O [0, 256), Q [256, 384), S slots [384, 448) and [448, 512)
 constexpr uint32_t kColQ = 256, kColS = 384;
 
+constexpr uint32_t kAhead = 2;  // S runs so many tiles ahead of O
+
 enum { B_VFULL = 0, B_VFREE = 4, B_SFULL = 8, B_SFREE = 10, B_SXFULL = 12, B_PXFULL = 14, B_PREADY = 16, B_PFREE = 18,
-       B_DONE = 20, B_COUNT = 21 };
+       B_SXFREE = 20, B_DONE = 22 };
 
 // ---------------------------------------------------------------------------------------
 // cluster shared memory
@@ -79,14 +85,13 @@ FP4KV_DEV uint32_t map_peer(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-FP4KV_DEV void st_peer_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 FP4KV_DEV void st_peer_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-FP4KV_DEV void mbar_arrive_peer(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// An arrival that only says "my loads have returned" (a releasing one would first wait for every
+// outstanding access of the thread: 1,000 cycles and more here).
+FP4KV_DEV void mbar_arrive_peer_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 FP4KV_DEV bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -110,7 +115,32 @@ FP4KV_DEV bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   }
   return __all_sync(0xffffffffu, ok);
 }
-FP4KV_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// This CTA's shared memory to the other's, completing on a barrier there; 16-byte units.
+FP4KV_DEV void bulk_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
+}
+FP4KV_DEV void st_async_f32(uint32_t dst, float v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(dst), "f"(v), "r"(bar) : "memory");
+}
+
+// two fp32 at once
+FP4KV_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+FP4KV_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+FP4KV_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+FP4KV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // A (fp16) from TMEM, B from shared memory
 FP4KV_DEV void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -143,21 +173,22 @@ FP4KV_DEV bool pair_any(int q, bool v) {
 // what a sequence has to do
 // ---------------------------------------------------------------------------------------
 struct Seq {
-  int nd;         // drafted tokens
-  int64_t pre;    // rows of the prefix
-  int64_t n_sel;  // entries before the drafts: the prefix, or the selection
-  int64_t tiles, groups;
+  int nd;          // drafted tokens
+  uint32_t pre;    // rows of the prefix (cap < 2^31)
+  uint32_t n_sel;  // entries before the drafts: the prefix, or the selection
+  uint32_t tiles, groups;
+  FP4KV_DEV int64_t work() const { return int64_t(tiles) * groups; }
 };
 FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
   Seq s;
   s.nd = p.n_draft ? max(0, min(p.n_draft[b], p.T)) : p.T;
-  s.pre = max(int64_t(0), min(int64_t(p.prefix_lens[b]), p.cap));
+  s.pre = static_cast<uint32_t>(max(int64_t(0), min(int64_t(p.prefix_lens[b]), p.cap)));
   s.n_sel = p.idx && s.pre > 0 ? p.top_k : s.pre;
   s.tiles = (s.n_sel + s.nd + kTile - 1) / kTile;
-  s.groups = (int64_t(s.nd) * p.H + kRows - 1) / kRows;
+  s.groups = (static_cast<uint32_t>(s.nd) * p.H + kRows - 1) / kRows;
   return s;
 }
-// Clusters in use for `total` tiles: at least tree_min_tiles() each.
+// Clusters in use for `total` tiles: at least min_tiles each.
 FP4KV_DEV int64_t clusters_used(int64_t total, int n_clusters, int min_tiles) {
   return max(int64_t(1), min(int64_t(n_clusters), (total + min_tiles - 1) / min_tiles));
 }
@@ -167,18 +198,17 @@ struct SegIter {
   int b;
   int64_t off, rem;  // tiles of sequence b already passed; tiles still to do
   Seq s;
-  int64_t g, tile0;
-  int nt;
+  uint32_t g, tile0, nt;
   FP4KV_DEV bool next(const TreeAttnParams& p) {
     if (rem <= 0) return false;
     s = seq_of(p, b);
-    while (off >= s.tiles * s.groups) {
-      off -= s.tiles * s.groups;
+    while (off >= s.work()) {
+      off -= s.work();
       s = seq_of(p, ++b);
     }
-    g = off / s.tiles;
-    tile0 = off - g * s.tiles;
-    nt = static_cast<int>(min(s.tiles - tile0, rem));
+    g = static_cast<uint32_t>(off / s.tiles);
+    tile0 = static_cast<uint32_t>(off - int64_t(g) * s.tiles);
+    nt = static_cast<uint32_t>(min(int64_t(s.tiles - tile0), rem));
     off += nt;
     rem -= nt;
     return true;
@@ -210,13 +240,13 @@ FP4KV_DEV void dequant_unit(uint8_t* stage, int row, int u, const uint4& c, uint
 // this thread's TMEM lane, 128 of its O columns, times a
 FP4KV_DEV void rescale_o(uint32_t addr, float a) {
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tmem_ld32(addr + 32 * c, r);
+  for (int c = 0; c < 8; ++c) {  // (16 at a time: the caller holds a tile's logits)
+    uint32_t r[16];
+    tmem_ld16(addr + 16 * c, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
-    tmem_st32(addr + 32 * c, r);
+    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
+    tmem_st16(addr + 16 * c, r);
   }
   tmem_st_wait();
 }
@@ -237,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
-  const int64_t cl = blockIdx.x >> 1;
+  const int cl = blockIdx.x >> 1;
   griddep_wait();
 
   // the smem alignment that the swizzled operands need (the same in both CTAs of a launch)
@@ -250,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     int64_t total = 0;
     for (int b = lane; b < p.B; b += 32) {
       const Seq s = seq_of(p, b);
-      total += s.tiles * s.groups;
+      total += s.work();
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -265,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       int64_t n = 0;
       if (b < p.B) {
         const Seq s = seq_of(p, b);
-        n = s.tiles * s.groups;
+        n = s.work();
       }
       int64_t incl = n;
 #pragma unroll
@@ -298,8 +328,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_SFULL + i], 1);
       mbar_init(&bars[B_SFREE + i], kSoftWarps);
-      mbar_init(&bars[B_SXFULL + i], kSoftWarps / 2);
-      mbar_init(&bars[B_PXFULL + i], kSoftWarps / 2);
+      mbar_init(&bars[B_SXFULL + i], 1);
+      mbar_init(&bars[B_SXFREE + i], kSoftWarps / 2);
+      mbar_init(&bars[B_PXFULL + i], 1);
       mbar_init(&bars[B_PREADY + i], kSoftWarps);
       mbar_init(&bars[B_PFREE + i], 2);
     }
@@ -344,27 +375,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
       const uint8_t* packed = p.packed + int64_t(it.b) * p.cap * (kD / 2) + 128 * rank;
       const uint8_t* scales = p.scales + int64_t(it.b) * p.cap * (kD / kGroup) + 16 * rank;
-      auto pos_of = [&](int i) -> int64_t {
-        const int64_t e = (it.tile0 + i) * kTile + row;
-        int64_t pos = -1;
+      auto pos_of = [&](uint32_t i) -> int32_t {
+        const uint32_t e = (it.tile0 + i) * kTile + row;
+        int32_t pos = -1;
         if (i < it.nt) {
           if (e < s.n_sel) {
-            pos = idx ? idx[e] : e;
-            if (pos >= s.pre) pos = -1;
+            pos = idx ? idx[e] : static_cast<int32_t>(e);
+            if (static_cast<uint32_t>(pos) >= s.pre) pos = -1;
           } else {
-            const int64_t j = e - s.n_sel;
-            if (j < s.nd && ((seen >> j) & 1) && s.pre + j < p.cap) pos = s.pre + j;
+            const uint32_t j = e - s.n_sel;
+            if (j < uint32_t(s.nd) && ((seen >> j) & 1) && int64_t(s.pre) + j < p.cap) pos = static_cast<int32_t>(s.pre + j);
           }
         }
         return pos;
       };
-      auto load = [&](int64_t pos) {
+      auto load = [&](int32_t pos) {
         RawRow r;
         r.c0 = r.c1 = make_uint4(0, 0, 0, 0);
         r.s0 = r.s1 = 0;
         if (pos >= 0) {
-          const uint8_t* c = packed + pos * (kD / 2) + 16 * u0;
-          const uint8_t* f = scales + pos * (kD / kGroup) + 2 * u0;
+          const uint8_t* c = packed + int64_t(pos) * (kD / 2) + 16 * u0;
+          const uint8_t* f = scales + int64_t(pos) * (kD / kGroup) + 2 * u0;
           r.c0 = ld_nc_v4(c);
           r.c1 = ld_nc_v4(c + 64);
           r.s0 = *reinterpret_cast<const uint16_t*>(f);
@@ -373,15 +404,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         return r;
       };
       RawRow r0 = load(pos_of(0)), r1 = load(pos_of(1));
-      int64_t p2 = pos_of(2);
+      int32_t p2 = pos_of(2);
       cluster_sync_all();  // start of the segment
-      for (int i = 0; i < it.nt && !aborted(); ++i) {
+      for (uint32_t i = 0; i < it.nt && !aborted(); ++i) {
         const RawRow cur = r0;
         r0 = r1;
         r1 = load(p2);
         p2 = pos_of(i + 3);
         const uint32_t m = n + i, st = m & (kStages - 1);
-        if (!warp_wait(&bars[B_VFREE + st], ((m >> 2) & 1) ^ 1)) {
+        // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
+        if (!__all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + st], ((m >> 2) & 1) ^ 1, 64))) {
           give_up();
           break;
         }
@@ -402,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     constexpr uint32_t kIdescO = umma_idesc(0u, kRows, kHalf, 0u, 1u);
     const uint64_t dvk = sw128_kmajor_desc(smem_u32(smem + kOffV));
     const uint64_t dvm = sw128_mnmajor_desc(smem_u32(smem + kOffV), kVChunk);
-    const uint64_t dp = sw128_kmajor_desc(smem_u32(smem + kOffP));
+    const uint64_t dp = sw64_kmajor_desc(smem_u32(smem + kOffP));
     auto scores = [&](uint32_t m) -> bool {
       const uint32_t st = m & (kStages - 1), sl = m & 1;
       if (!warp_wait(&bars[B_VFULL + st], (m >> 2) & 1) || !warp_wait(&bars[B_SFREE + sl], ((m >> 1) & 1) ^ 1)) return false;
@@ -423,16 +455,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     while (it.next(p)) {
       cluster_sync_all();  // start
       tc_fence_after();
-      bool ok = !aborted() && scores(n);
-      for (int i = 0; ok && i < it.nt; ++i) {
+      bool ok = !aborted();
+      for (uint32_t i = 0; ok && i < kAhead && i < it.nt; ++i) ok = scores(n + i);
+      for (uint32_t i = 0; ok && i < it.nt; ++i) {
         const uint32_t m = n + i, st = m & (kStages - 1), sl = m & 1;
-        if (i + 1 < it.nt && !scores(m + 1)) ok = false;
+        if (i + kAhead < it.nt && !scores(m + kAhead)) ok = false;
         if (ok && !warp_wait(&bars[B_PREADY + sl], (m >> 1) & 1)) ok = false;
         if (ok && lane == 0) {
           tc_fence_after();
           const uint64_t a0 = dp + ((sl * kPBytes) >> 4), b0 = dvm + ((st * kVBytes) >> 4);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) umma_f16(tmem, a0 + 2 * k, b0 + ((2048 * k) >> 4), kIdescO, i > 0 || k > 0);
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_f16(tmem, a0 + ((kPBytes / 2 * (k >> 1)) >> 4) + 2 * (k & 1), b0 + ((2048 * k) >> 4), kIdescO, i > 0 || k > 0);
           umma_commit(&bars[B_VFREE + st]);
           umma_commit_pair(&bars[B_PFREE + sl]);
         }
@@ -457,15 +491,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     const uint32_t peer_smem = map_peer(smem_u32(smem), peer);
     while (it.next(p)) {
       const Seq& s = it.s;
-      const int64_t live_rows = int64_t(s.nd) * p.H - it.g * kRows;  // of this item
-      const int64_t row0 = int64_t(it.b) * p.T * p.H + it.g * kRows;
+      const int live_rows = s.nd * p.H - static_cast<int>(it.g) * kRows;  // of this item (and behind)
+      const int64_t row0 = int64_t(it.b) * p.T * p.H + int64_t(it.g) * kRows;
       // ---- Q: bf16 -> fp16 times a power of two, through shared memory into TMEM ----
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint4 v[8][2];
+      for (int half = 0; half < 4; ++half) {
+        uint4 v[4][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = warp + 8 * (8 * half + k);
+        for (int k = 0; k < 4; ++k) {
+          const int r = warp + 8 * (4 * half + k);
           v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
           if (r < live_rows) {
             const uint16_t* src = p.q + (row0 + r) * kD + 8 * lane;
@@ -474,8 +508,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = warp + 8 * (8 * half + k);
+        for (int k = 0; k < 4; ++k) {
+          const int r = warp + 8 * (4 * half + k);
           uint32_t m2 = 0;
           m2 = __vmaxu2(v[k][0].x & 0x7fff7fffu, v[k][0].y & 0x7fff7fffu);
           m2 = __vmaxu2(m2, __vmaxu2(v[k][0].z & 0x7fff7fffu, v[k][0].w & 0x7fff7fffu));
@@ -484,7 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
           int e = 0;  // the power of two that brings the row's maximum into [2^14, 2^15)
           if (m != 0) e = max(-126, min(127, 14 - max(-126, int(m >> 7) - 127)));
-          const float up = __uint_as_float(uint32_t(127 + e) << 23);
+          // (a negative scale goes into q's sign: the factor of the logits is positive)
+          const float up = copysignf(__uint_as_float(uint32_t(127 + e) << 23), p.sm_scale);
           const uint4 own_half = rank ? v[k][1] : v[k][0];
           const uint32_t w[4] = {own_half.x, own_half.y, own_half.z, own_half.w};
           uint32_t f[4];
@@ -493,8 +528,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             f[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
           *reinterpret_cast<uint4*>(smem + kOffQ + r * 512 + ((lane ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
           if (lane == 0)
-            sC[r] = p.sm_scale * kLog2e * __uint_as_float(uint32_t(127 - e / 2) << 23) *
-                    __uint_as_float(uint32_t(127 - (e - e / 2)) << 23);
+            sC[r] = fmaxf(fabsf(p.sm_scale) * kLog2e * __uint_as_float(uint32_t(127 - e / 2) << 23) *
+                              __uint_as_float(uint32_t(127 - (e - e / 2)) << 23),
+                          2e-38f);  // (above zero: a masked -inf stays -inf)
         }
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -516,37 +552,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
 
       bool ok = true;
       if (own) {
-        const int64_t grow = it.g * kRows + R;
         uint64_t rmask = 0;  // the drafts that this row's token sees
         if (R < live_rows) {
-          rmask = p.tree_mask[int64_t(it.b) * p.T + grow / p.H];
-          const int64_t nv = min(int64_t(s.nd), p.cap - s.pre);
+          rmask = p.tree_mask[int64_t(it.b) * p.T + (it.g * kRows + R) / uint32_t(p.H)];
+          const int64_t nv = min(int64_t(s.nd), p.cap - int64_t(s.pre));
           if (nv < 64) rmask &= (uint64_t(1) << nv) - 1;
         }
         const float c = sC[R];
         const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
-        auto entry_ok = [&](int i) -> bool {  // entry 32 h + lane of tile i lies in the prefix
-          const int64_t e = (it.tile0 + i) * kTile + 32 * h + lane;
+        auto entry_ok = [&](uint32_t i) -> bool {  // entry 32 h + lane of tile i lies in the prefix
+          const uint32_t e = (it.tile0 + i) * kTile + 32 * h + lane;
           if (i >= it.nt || e >= s.n_sel) return false;
-          if (!idx) return true;
-          const int64_t pos = idx[e];
-          return pos >= 0 && pos < s.pre;
+          return !idx || static_cast<uint32_t>(idx[e]) < s.pre;
         };
         bool e_ok = entry_ok(0);
-        float ref = -INFINITY, limit = -INFINITY, m6 = INFINITY, l = 0.0f;
+        float ref = -INFINITY, limit = -INFINITY, m6 = INFINITY;
+        uint64_t l2 = 0;  // the row's sum over even and odd columns
+        const uint64_t c2 = pack2(c, c);
+        const bool arms = h == 0 && (q & 1) == 0 && lane == 0;
         // a wait that ran out ends the loop of both warps of a row at the next vote
         bool dead = false;
-        for (int i = 0; i < it.nt; ++i) {
+        for (uint32_t i = 0; i < it.nt; ++i) {
           const uint32_t m = n + i, sl = m & 1;
           dead = dead || aborted();
+          if (arms) mbar_arrive_expect_tx(&bars[B_SXFULL + sl], kSxBytes);
           uint32_t vis = __ballot_sync(0xffffffffu, e_ok);
           e_ok = entry_ok(i + 1);
-          const int64_t dd = (it.tile0 + i) * kTile + 32 * h - s.n_sel;
-          if (dd >= 0) {
-            if (dd < 64) vis |= uint32_t(rmask >> dd);
-          } else if (dd > -32) {
-            vis |= uint32_t(rmask << -dd);
-          }
+          const uint32_t e0 = (it.tile0 + i) * kTile + 32 * h;
+          if (e0 + 32 > s.n_sel)  // drafts among the columns
+            vis |= e0 >= s.n_sel ? (e0 - s.n_sel < 64 ? uint32_t(rmask >> (e0 - s.n_sel)) : 0u) : uint32_t(rmask << (s.n_sel - e0));
           dead = dead || !warp_wait(&bars[B_SFULL + sl], (m >> 1) & 1);
           tc_fence_after();
           uint32_t r[32];
@@ -556,26 +590,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_SFREE + sl]);
           dead = dead || !warp_wait_cluster(&bars[B_SXFULL + sl], (m >> 1) & 1);
-          const float4* sx = reinterpret_cast<const float4*>(smem + kOffSx + sl * kSxBytes) + 8 * h * 64 + rl;
-          float z[32];
+          const float4* sx = reinterpret_cast<const float4*>(smem + kOffSx + sl * kSxBytes + 4096 * (2 * (q & 1) + h)) + lane;
+          uint64_t z[16];  // logits over c
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float4 f = sx[64 * k];
-            z[4 * k] = (__uint_as_float(r[4 * k]) + f.x) * c;
-            z[4 * k + 1] = (__uint_as_float(r[4 * k + 1]) + f.y) * c;
-            z[4 * k + 2] = (__uint_as_float(r[4 * k + 2]) + f.z) * c;
-            z[4 * k + 3] = (__uint_as_float(r[4 * k + 3]) + f.w) * c;
+            const float4 f = sx[32 * k];
+            z[2 * k] = add2(pack2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), pack2(f.x, f.y));
+            z[2 * k + 1] = add2(pack2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), pack2(f.z, f.w));
           }
-          if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+          float mx = -INFINITY;
+          if (__all_sync(0xffffffffu, vis == 0xffffffffu)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((vis >> k) & 1)) z[k] = -INFINITY;
+            for (int k = 0; k < 16; ++k) {
+              float z0, z1;
+              unpack2(z[k], z0, z1);
+              mx = fmaxf(mx, fmaxf(z0, z1));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float z0, z1;
+              unpack2(z[k], z0, z1);
+              z0 = (vis >> (2 * k)) & 1 ? z0 : -INFINITY;
+              z1 = (vis >> (2 * k + 1)) & 1 ? z1 : -INFINITY;
+              z[k] = pack2(z0, z1);
+              mx = fmaxf(mx, fmaxf(z0, z1));
+            }
           }
-          float mx = z[0];
-#pragma unroll
-          for (int k = 1; k < 32; ++k) mx = fmaxf(mx, z[k]);
+          mx *= c;
           float a = 1.0f;
-          if (pair_any(q, mx > limit || dead)) {  // a reference of these 32 rows moves
+          const bool moves = pair_any(q, mx > limit || dead);
+          // (the vote needs the loaded values, so every lane's loads from the slot have returned)
+          if (lane == 0) mbar_arrive_peer_relaxed(peer_smem + kOffBar + 8 * (B_SXFREE + sl));
+          if (moves) {  // a reference of these 32 rows moves
             if (pair_any(q, dead)) {
               dead = true;
               break;
@@ -589,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
               ref = to;
               limit = to + kMoveLog2;
               m6 = to - kPLog2;
-              l *= a;
+              l2 = fma2(l2, pack2(a, a), 0);
             }
             if (i == 0) a = 1.0f;  // (O starts with this tile)
             if (__any_sync(0xffffffffu, a != 1.0f)) {
@@ -600,36 +647,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           }
           // P's slot is free in both CTAs
           dead = dead || !warp_wait_cluster(&bars[B_PFREE + sl], ((m >> 1) & 1) ^ 1);
-          if (h == 0) st_peer_f32(peer_smem + kOffAx + 4 * (64 * sl + rl), a);
-          const uint32_t prow = kOffP + sl * kPBytes + R * 128;
+          const uint32_t px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + sl);
+          if (h == 0) st_async_f32(peer_smem + kOffAx + 4 * (64 * sl + rl), a, px_bar);
+          const uint32_t pw = kOffP + sl * kPBytes + h * (kPBytes / 2) + 32 * q * 64;  // this warp's 2 KiB
+          uint8_t* prow = smem + pw + lane * 64;
+          const uint64_t m62 = pack2(-m6, -m6);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float e0 = ex2(z[8 * u + 2 * k] - m6), e1 = ex2(z[8 * u + 2 * k + 1] - m6);
-              l += e0 + e1;
+              float z0, z1;
+              unpack2(fma2(z[4 * u + k], c2, m62), z0, z1);
+              const float e0 = ex2(z0), e1 = ex2(z1);
+              l2 = add2(l2, pack2(e0, e1));
               w[k] = pack_f16x2(e0, e1);
             }
-            const uint32_t at = prow + (((4 * h + u) ^ (R & 7)) << 4);
-            const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(smem + at) = w4;
-            st_peer_v4(peer_smem + at, w4);
+            *reinterpret_cast<uint4*>(prow + ((u ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          fence_proxy_async_all();
+          fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
+            bulk_peer(peer_smem + pw, smem_u32(smem) + pw, kPBytes / 8, px_bar);
             mbar_arrive(&bars[B_PREADY + sl]);
-            mbar_arrive_peer(peer_smem + kOffBar + 8 * (B_PXFULL + sl));
           }
         }
         ok = !dead;
         // the row's sum; reference and sum to both CTAs
-        sPair[128 + 64 * h + rl] = l;
+        float l, l1;
+        unpack2(l2, l, l1);
+        l += l1;
+        if (h == 1) sPair[128 + rl] = l;
         pair_sync(q);
         if (h == 0) {
-          l += sPair[128 + 64 + rl];
+          l += sPair[128 + rl];
           sM[R] = ref;
           sL[R] = l;
           st_peer_f32(peer_smem + kOffM + 4 * R, ref);
@@ -639,6 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         // P(j)'s rows from the other CTA have arrived, O's rows follow a moved reference
         auto take_p = [&](uint32_t m) -> bool {
           const uint32_t sl = m & 1;
+          if (h == 0 && (q & 1) == 0 && lane == 0) mbar_arrive_expect_tx(&bars[B_PXFULL + sl], kPBytes / 2 + 256);
           if (!warp_wait_cluster(&bars[B_PXFULL + sl], (m >> 1) & 1)) return false;
           const float a = sAx[64 * sl + rl];
           if (__any_sync(0xffffffffu, a != 1.0f)) {
@@ -646,13 +699,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             tc_fence_after();
             rescale_o(o_addr, a);
           }
-          fence_proxy_async_all();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_PREADY + sl]);
           return true;
         };
-        for (int i = 0; i < it.nt && !aborted(); ++i) {
+        for (uint32_t i = 0; i < it.nt && !aborted(); ++i) {
           const uint32_t m = n + i, sl = m & 1;
           if (!warp_wait(&bars[B_SFULL + sl], (m >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
@@ -662,12 +714,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_SFREE + sl]);
-          const uint32_t dst = peer_smem + kOffSx + sl * kSxBytes + 16 * (8 * h * 64 + rl);
+          // (the receiver has read S(m - 2): its slot and its staging here are free)
+          if (!warp_wait_cluster(&bars[B_SXFREE + sl], ((m >> 1) & 1) ^ 1)) { ok = false; break; }
+          const uint32_t wo = sl * kSxBytes + 4096 * (2 * (q & 1) + h);
+          uint4* st = reinterpret_cast<uint4*>(smem + kOffSt + wo) + lane;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            st_peer_v4(dst + 1024 * k, make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]));
+          for (int k = 0; k < 8; ++k) st[32 * k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_peer(peer_smem + kOffBar + 8 * (B_SXFULL + sl));
+          if (lane == 0) {
+            bulk_peer(peer_smem + kOffSx + wo, smem_u32(smem + kOffSt) + wo, 4096,
+                      peer_smem + kOffBar + 8 * (B_SXFULL + sl));
+          }
+          // (not behind S(m + 2)'s: S(m + 3) is issued after O(m + 1), which waits for this)
           if (i > 0 && !take_p(m - 1)) { ok = false; break; }
         }
         if (ok) ok = !aborted() && take_p(n + it.nt - 1);
@@ -684,7 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       const float l = sL[R], ref = sM[R];
       const bool whole = it.tile0 == 0 && it.nt == s.tiles;
       const bool live = R < live_rows;
-      const int64_t slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
+      const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -705,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + (slot * kRows + R) * kD + ch);
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + int64_t(slot * kRows + R) * kD + ch);
 #pragma unroll
           for (int k = 0; k < 8; ++k) __stcg(dst + k, make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]));
         }
@@ -737,9 +796,9 @@ __global__ void __launch_bounds__(kD / 4) k_tree_merge(const TreeAttnParams p) {
   const int b = static_cast<int>(row / (p.T * p.H));
   const int rr = static_cast<int>(row - int64_t(b) * p.T * p.H);
   const Seq s = seq_of(p, b);
-  if (rr >= int64_t(s.nd) * p.H) return;
+  if (rr >= s.nd * p.H) return;
   const int64_t total = p.first_tile[p.B], used = clusters_used(total, p.n_clusters, p.min_tiles);
-  const int64_t x = p.first_tile[b] + (rr / kRows) * s.tiles;
+  const int64_t x = p.first_tile[b] + int64_t(rr / kRows) * s.tiles;
   // the cluster of tile x: the largest i with floor(total i / used) <= x
   const int64_t c0 = ((x + 1) * used - 1) / total, c1 = ((x + s.tiles) * used - 1) / total;
   if (c0 == c1) return;
