@@ -17,15 +17,15 @@
 // half row of V feeds N = 64 and N = 256 products whose other operand is 128 rows deep. (The transposed
 // form with all channels in one CTA, O^T of 512 x 64, reads shared memory 1.6 times as much per flop.)
 //
-// A CTA (17 warps):
-//  * warps 8-15 dequantize: a tile's 64 half rows to fp16 (exact) in 128-byte-swizzled 64-channel
+// A CTA (25 warps):
+//  * warps 16-23 dequantize: a tile's 64 half rows to fp16 (exact) in 128-byte-swizzled 64-channel
 //    chunks, K-major B operand of S and MN-major B operand of O; four stages, loads two tiles ahead;
-//  * warp 16 issues S(t + 2) (A = Q in TMEM), then O += P(t) V(t) (A = P in shared memory);
-//  * warps 0-7 own TMEM lane quarter w % 4 (query rows) and column half w / 4. Those of the CTA's
+//  * warp 24 issues S(t + 2) (A = Q in TMEM), then O += P(t) V(t) (A = P in shared memory);
+//  * warps 0-15 own TMEM lane quarter w % 4 (query rows) and column quarter w / 4. Those of the CTA's
 //    own rows add the two parts of S, keep reference and sum in registers (lane = query row), and
 //    write P; the others send their part of S over and take P's arrival.
-// What crosses over goes by bulk copies that complete on the receiver's barrier: 4 KiB of S per warp
-// and tile, 2 KiB of P. (Stores to the other CTA's memory, followed by a releasing arrival, held up the
+// What crosses over goes by bulk copies that complete on the receiver's barrier: 2 KiB of S per warp
+// and tile, 1 KiB of P. (Stores to the other CTA's memory, followed by a releasing arrival, held up the
 // SM's other shared-memory instructions: 6,300 cycles a tile. The link moves 20 bytes a cycle each way.)
 // Numerics: q as fp16 times a power of two per row (exact within 2^29 of the row's maximum), v exact
 // in fp16, S and O in fp32. The reference m moves only when a logit passes it by 2^9 (log2 domain),
@@ -44,14 +44,15 @@ constexpr int kD = 512, kHalf = 256;
 constexpr int kRows = 128;  // query rows of an item
 constexpr int kTile = 64;   // cache rows of a tile
 constexpr int kStages = 4;
-constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16;
-constexpr int kThreads = 32 * 17;
+constexpr int kSoftWarps = 16, kDeqWarps = 8, kMmaWarp = 24;
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole warpgroups: registers move between them)
+constexpr int kCols = kTile / 2;  // columns of S per softmax warp
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMoveLog2 = 9.0f, kHeadroomLog2 = 3.0f, kPLog2 = 6.0f;
 
 constexpr uint32_t kVBytes = kTile * kHalf * 2;   // 32 KiB: 4 chunks of [64 rows][128 B]
 constexpr uint32_t kVChunk = kTile * 128;
-constexpr uint32_t kPBytes = kRows * 128;         // [2 halves of 32 cache rows][128 query rows][64 B] fp16
+constexpr uint32_t kPBytes = kRows * 128;         // [2 column halves][128 query rows][64 B] fp16
 constexpr uint32_t kSxBytes = 64 * kTile * 4;     // [4 warps][8 column fours][32 query rows][4] fp32
 constexpr uint32_t kOffV = 0;
 constexpr uint32_t kOffP = kOffV + kStages * kVBytes;
@@ -60,13 +61,13 @@ constexpr uint32_t kOffSt = kOffSx + 2 * kSxBytes;  // S on its way out, [2 tile
 constexpr uint32_t kOffQ = kOffP;                 // Q's way into TMEM: [128 rows][512 B] over P and Sx
 static_assert(2 * kPBytes + 2 * kSxBytes == kRows * kHalf * 2, "Q staging");
 constexpr uint32_t kOffBar = kOffSt + 2 * kSxBytes;
-constexpr uint32_t kOffMisc = kOffBar + 192;
+constexpr uint32_t kOffMisc = kOffBar + 208;
 constexpr uint32_t kOffC = kOffBar + 256;         // [128] logit scale (log2 domain) per query row
+constexpr uint32_t kOffMLx = kOffC;               // [2][64] (C is read before the start): the other CTA's rows' reference, sum
 constexpr uint32_t kOffAx = kOffC + 512;          // [2][64] rescale factors of the other CTA's rows
-constexpr uint32_t kOffM = kOffAx + 512;          // [128] reference at the end
-constexpr uint32_t kOffL = kOffM + 512;           // [128] sum at the end
-constexpr uint32_t kOffPair = kOffL + 512;        // [3][64] exchange between a row's two threads: maxima, one sum
-constexpr uint32_t kSmem = kOffPair + 768;
+constexpr uint32_t kOffPair = kOffAx + 512;       // [4][64] exchange between a row's four threads
+constexpr uint32_t kOffRef = kOffPair + 1024;     // [2][64] reference after the last tile of either parity
+constexpr uint32_t kSmem = kOffRef + 512;
 static_assert(kSmem <= 232448, "shared memory");
 
 // TMEM columns: O [0, 256), Q [256, 384), S slots [384, 448) and [448, 512)
@@ -75,7 +76,7 @@ constexpr uint32_t kColQ = 256, kColS = 384;
 constexpr uint32_t kAhead = 2;  // S runs so many tiles ahead of O
 
 enum { B_VFULL = 0, B_VFREE = 4, B_SFULL = 8, B_SFREE = 10, B_SXFULL = 12, B_PXFULL = 14, B_PREADY = 16, B_PFREE = 18,
-       B_SXFREE = 20, B_DONE = 22 };
+       B_SXFREE = 20, B_REF = 22, B_DONE = 24 };
 
 // ---------------------------------------------------------------------------------------
 // cluster shared memory
@@ -142,32 +143,63 @@ FP4KV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// A (fp16) from TMEM, B from shared memory
-FP4KV_DEV void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One lane of a converged warp.
+FP4KV_DEV uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+// The MMA and commit wrappers below are called by the whole warp; the lane with `go` issues. The
+// operands stay warp-uniform that way: inside a branch of one lane each MMA took 100 cycles to issue.
+// D[tmem] (+)= A * B^T, fp16, A from TMEM, B from shared memory
+FP4KV_DEV void umma_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
+      "{\n .reg .pred p, g;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 g, %5, 0;\n"
+      " @g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go) : "memory");
+}
+// the same, A from shared memory
+FP4KV_DEV void umma_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, g;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 g, %5, 0;\n"
+      " @g tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go) : "memory");
+}
+FP4KV_DEV void commit_if(uint32_t go, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred g;\n setp.ne.b32 g, %1, 0;\n"
+      " @g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+      ::"r"(smem_u32(bar)), "r"(go) : "memory");
 }
 // Arrive on the mbarrier at this offset in both CTAs of the cluster.
-FP4KV_DEV void umma_commit_pair(uint64_t* bar) {
+FP4KV_DEV void commit_pair_if(uint32_t go, uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+      "{\n .reg .pred g;\n setp.ne.b32 g, %2, 0;\n"
+      " @g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}"
+      ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "r"(go) : "memory");
 }
 FP4KV_DEV float ex2(float x) {  // a few units in the last place; results below 2^-126 flushed to zero
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The two warps (column halves) of a lane quarter.
-FP4KV_DEV void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(2 + q) : "memory"); }
-FP4KV_DEV bool pair_any(int q, bool v) {
+// The two warps (column halves) of a lane quarter in one set.
+FP4KV_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(2 + id) : "memory"); }
+FP4KV_DEV bool pair_any(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.or.pred po, %2, 64, pi;\n selp.u32 %0, 1, 0, po;\n}"
-      : "=r"(r) : "r"(v ? 1u : 0u), "r"(2 + q) : "memory");
+      : "=r"(r) : "r"(v ? 1u : 0u), "r"(2 + id) : "memory");
   return r != 0;
 }
+// The four warps of a lane quarter.
+FP4KV_DEV void quad_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(10 + q) : "memory"); }
+// Registers move between warpgroups: 896 threads are launched with 72 each (16 x 88 + 8 x 48 + 4 x 56
+// = 28 x 72 registers per lane).
+template <int N>
+FP4KV_DEV void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+FP4KV_DEV void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ---------------------------------------------------------------------------------------
 // what a sequence has to do
@@ -256,9 +288,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   float* sC = reinterpret_cast<float*>(smem + kOffC);
   float* sAx = reinterpret_cast<float*>(smem + kOffAx);
-  float* sM = reinterpret_cast<float*>(smem + kOffM);
-  float* sL = reinterpret_cast<float*>(smem + kOffL);
+  const float* sMLx = reinterpret_cast<const float*>(smem + kOffMLx);
   float* sPair = reinterpret_cast<float*>(smem + kOffPair);
+  float* sRef = reinterpret_cast<float*>(smem + kOffRef);
   int64_t* s_off = reinterpret_cast<int64_t*>(smem + kOffMisc);  // the range's start: tiles into sequence s_b
   int64_t* s_rem = s_off + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 16);
@@ -327,11 +359,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_SFULL + i], 1);
-      mbar_init(&bars[B_SFREE + i], kSoftWarps);
+      mbar_init(&bars[B_SFREE + i], kSoftWarps / 2);
       mbar_init(&bars[B_SXFULL + i], 1);
-      mbar_init(&bars[B_SXFREE + i], kSoftWarps / 2);
+      mbar_init(&bars[B_SXFREE + i], kSoftWarps / 4);
       mbar_init(&bars[B_PXFULL + i], 1);
-      mbar_init(&bars[B_PREADY + i], kSoftWarps);
+      mbar_init(&bars[B_PREADY + i], kSoftWarps / 2);
+      mbar_init(&bars[B_REF + i], 2);
       mbar_init(&bars[B_PFREE + i], 2);
     }
     mbar_init(&bars[B_DONE], 1);
@@ -363,6 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
 
   if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ------------------------------ load and dequantize ------------------------------
+    fewer_registers<48>();
     // Eight lanes take eight rows (distinct swizzle phases: no store conflicts), four units each.
     const int row = 8 * (warp - kSoftWarps) + (lane & 7), u0 = lane >> 3;
     while (it.next(p)) {
@@ -375,25 +409,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
       const uint8_t* packed = p.packed + int64_t(it.b) * p.cap * (kD / 2) + 128 * rank;
       const uint8_t* scales = p.scales + int64_t(it.b) * p.cap * (kD / kGroup) + 16 * rank;
+      // this thread's row of tile i: a position, which is checked only when it is used (it may still be
+      // on its way from the selection)
       auto pos_of = [&](uint32_t i) -> int32_t {
         const uint32_t e = (it.tile0 + i) * kTile + row;
-        int32_t pos = -1;
-        if (i < it.nt) {
-          if (e < s.n_sel) {
-            pos = idx ? idx[e] : static_cast<int32_t>(e);
-            if (static_cast<uint32_t>(pos) >= s.pre) pos = -1;
-          } else {
-            const uint32_t j = e - s.n_sel;
-            if (j < uint32_t(s.nd) && ((seen >> j) & 1) && int64_t(s.pre) + j < p.cap) pos = static_cast<int32_t>(s.pre + j);
-          }
-        }
-        return pos;
+        if (i >= it.nt) return -1;
+        if (e < s.n_sel) return idx ? idx[e] : static_cast<int32_t>(e);
+        const uint32_t j = e - s.n_sel;
+        return j < uint32_t(s.nd) && ((seen >> j) & 1) && int64_t(s.pre) + j < p.cap ? static_cast<int32_t>(s.pre + j) : -1;
       };
-      auto load = [&](int32_t pos) {
-        RawRow r;
+      auto load = [&](RawRow& r, uint32_t i, int32_t pos) {
+        const bool sel = (it.tile0 + i) * kTile + row < s.n_sel;
         r.c0 = r.c1 = make_uint4(0, 0, 0, 0);
         r.s0 = r.s1 = 0;
-        if (pos >= 0) {
+        if (static_cast<uint32_t>(pos) < (sel ? s.pre : 0x80000000u)) {
           const uint8_t* c = packed + int64_t(pos) * (kD / 2) + 16 * u0;
           const uint8_t* f = scales + int64_t(pos) * (kD / kGroup) + 2 * u0;
           r.c0 = ld_nc_v4(c);
@@ -401,89 +430,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           r.s0 = *reinterpret_cast<const uint16_t*>(f);
           r.s1 = *reinterpret_cast<const uint16_t*>(f + 8);
         }
-        return r;
       };
-      RawRow r0 = load(pos_of(0)), r1 = load(pos_of(1));
-      int32_t p2 = pos_of(2);
+      RawRow ra, rb, rc;  // tiles i, i + 1, i + 2 (each reloaded in place: a copy would wait for its loads)
+      load(ra, 0, pos_of(0));
+      load(rb, 1, pos_of(1));
+      load(rc, 2, pos_of(2));
+      int32_t pos = pos_of(3);
+      bool ok = !aborted();
       cluster_sync_all();  // start of the segment
-      for (uint32_t i = 0; i < it.nt && !aborted(); ++i) {
-        const RawRow cur = r0;
-        r0 = r1;
-        r1 = load(p2);
-        p2 = pos_of(i + 3);
+      auto tile = [&](RawRow& r, uint32_t i) {
+        if (!ok || i >= it.nt) return;
         const uint32_t m = n + i, st = m & (kStages - 1);
         // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
-        if (!__all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + st], ((m >> 2) & 1) ^ 1, 64))) {
-          give_up();
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + st], ((m >> 2) & 1) ^ 1, 64));
+        if (!ok) return;
         uint8_t* stage = smem + kOffV + st * kVBytes;
-        dequant_unit(stage, row, u0, cur.c0, cur.s0);
-        dequant_unit(stage, row, u0 + 4, cur.c1, cur.s1);
+        dequant_unit(stage, row, u0, r.c0, r.s0);
+        dequant_unit(stage, row, u0 + 4, r.c1, r.s1);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_VFULL + st]);
+        load(r, i + 3, pos);
+        pos = pos_of(i + 4);
+      };
+      for (uint32_t i = 0; ok && i < it.nt; i += 3) {
+        tile(ra, i);
+        tile(rb, i + 1);
+        tile(rc, i + 2);
       }
+      if (!ok) give_up();
       n += it.nt;
       __syncwarp();
       cluster_sync_all();  // end of the segment
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------ MMA issue ------------------------------
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------ MMA issue (one warp; its warpgroup's others idle) ------------------------------
+    fewer_registers<56>();
     constexpr uint32_t kIdescS = umma_idesc(0u, kRows, kTile, 0u, 0u);
     constexpr uint32_t kIdescO = umma_idesc(0u, kRows, kHalf, 0u, 1u);
     const uint64_t dvk = sw128_kmajor_desc(smem_u32(smem + kOffV));
     const uint64_t dvm = sw128_mnmajor_desc(smem_u32(smem + kOffV), kVChunk);
     const uint64_t dp = sw64_kmajor_desc(smem_u32(smem + kOffP));
+    const uint32_t go = elect_lane();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     auto scores = [&](uint32_t m) -> bool {
       const uint32_t st = m & (kStages - 1), sl = m & 1;
       if (!warp_wait(&bars[B_VFULL + st], (m >> 2) & 1) || !warp_wait(&bars[B_SFREE + sl], ((m >> 1) & 1) ^ 1)) return false;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint64_t b0 = dvk + ((st * kVBytes) >> 4);
-        const uint32_t d = tmem + kColS + kTile * sl;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c)
+      tc_fence_after();
+      const uint64_t b0 = dvk + ((st * kVBytes) >> 4);
+      const uint32_t d = tm + kColS + kTile * sl;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f16_ts(d, tmem + kColQ + 32 * c + 8 * k, b0 + ((c * kVChunk) >> 4) + 2 * k, kIdescS, (c | k) != 0);
-        umma_commit(&bars[B_SFULL + sl]);
-      }
-      __syncwarp();
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_ts(go, d, tm + kColQ + 32 * c + 8 * k, b0 + ((c * kVChunk) >> 4) + 2 * k, kIdescS, (c | k) != 0);
+      commit_if(go, &bars[B_SFULL + sl]);
       return true;
     };
     while (it.next(p)) {
       cluster_sync_all();  // start
       tc_fence_after();
+      if (warp != kMmaWarp) {
+        cluster_sync_all();
+        continue;
+      }
       bool ok = !aborted();
       for (uint32_t i = 0; ok && i < kAhead && i < it.nt; ++i) ok = scores(n + i);
       for (uint32_t i = 0; ok && i < it.nt; ++i) {
         const uint32_t m = n + i, st = m & (kStages - 1), sl = m & 1;
         if (i + kAhead < it.nt && !scores(m + kAhead)) ok = false;
         if (ok && !warp_wait(&bars[B_PREADY + sl], (m >> 1) & 1)) ok = false;
-        if (ok && lane == 0) {
+        if (ok) {
           tc_fence_after();
           const uint64_t a0 = dp + ((sl * kPBytes) >> 4), b0 = dvm + ((st * kVBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            umma_f16(tmem, a0 + ((kPBytes / 2 * (k >> 1)) >> 4) + 2 * (k & 1), b0 + ((2048 * k) >> 4), kIdescO, i > 0 || k > 0);
-          umma_commit(&bars[B_VFREE + st]);
-          umma_commit_pair(&bars[B_PFREE + sl]);
+            umma_ss(go, tm, a0 + ((kPBytes / 2 * (k >> 1)) >> 4) + 2 * (k & 1), b0 + ((2048 * k) >> 4), kIdescO, i > 0 || k > 0);
+          commit_if(go, &bars[B_VFREE + st]);
+          commit_pair_if(go, &bars[B_PFREE + sl]);
         }
-        __syncwarp();
-        ok = ok && !aborted();
       }
       if (!ok) give_up();
       n += it.nt;
       __syncwarp();
       cluster_sync_all();  // end
     }
-    if (lane == 0) umma_commit(&bars[B_DONE]);  // nothing is in flight when TMEM is released
-    __syncwarp();
-    if (!warp_wait(&bars[B_DONE], 0)) give_up();
+    if (warp == kMmaWarp) {
+      commit_if(go, &bars[B_DONE]);  // nothing is in flight when TMEM is released
+      __syncwarp();
+      if (!warp_wait(&bars[B_DONE], 0)) give_up();
+    }
   } else {
     // ------------------------------ softmax ------------------------------
-    const int q = warp & 3, h = warp >> 2;
+    // Own rows: warps 0-7 take the even tiles (of all that the cluster works on), 8-15 the odd ones:
+    // every slot that a set uses is its own, and one set's waits overlap the other's arithmetic.
+    more_registers<88>();
+    const int q = warp & 3, h4 = warp >> 2, h = h4 & 1;
+    const uint32_t sl = warp >> 3;
+    const int pair = 4 * static_cast<int>(sl) + q;
     const int R = 32 * q + lane, rl = R & 63;  // query row of the item, and within its half
     const bool own = static_cast<uint32_t>(q >> 1) == rank;
     const uint32_t lane_addr = tmem + (uint32_t(32 * q) << 16);
@@ -495,11 +539,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       const int64_t row0 = int64_t(it.b) * p.T * p.H + int64_t(it.g) * kRows;
       // ---- Q: bf16 -> fp16 times a power of two, through shared memory into TMEM ----
 #pragma unroll 1
-      for (int half = 0; half < 4; ++half) {
+      for (int part = 0; part < 2; ++part) {
         uint4 v[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = warp + 8 * (4 * half + k);
+          const int r = warp + kSoftWarps * (4 * part + k);
           v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
           if (r < live_rows) {
             const uint16_t* src = p.q + (row0 + r) * kD + 8 * lane;
@@ -509,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = warp + 8 * (4 * half + k);
+          const int r = warp + kSoftWarps * (4 * part + k);
           uint32_t m2 = 0;
           m2 = __vmaxu2(v[k][0].x & 0x7fff7fffu, v[k][0].y & 0x7fff7fffu);
           m2 = __vmaxu2(m2, __vmaxu2(v[k][0].z & 0x7fff7fffu, v[k][0].w & 0x7fff7fffu));
@@ -533,24 +577,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
                           2e-38f);  // (above zero: a masked -inf stays -inf)
         }
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 f = *reinterpret_cast<const uint4*>(smem + kOffQ + R * 512 + (((16 * h + 8 * c + k) ^ (R & 7)) << 4));
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 f = *reinterpret_cast<const uint4*>(smem + kOffQ + R * 512 + (((8 * h4 + 4 * c + k) ^ (R & 7)) << 4));
           w[4 * k] = f.x; w[4 * k + 1] = f.y; w[4 * k + 2] = f.z; w[4 * k + 3] = f.w;
         }
-        tmem_st32(lane_addr + kColQ + 64 * h + 32 * c, w);
+        tmem_st16(lane_addr + kColQ + 32 * h4 + 16 * c, w);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
+      const float c = sC[R];
       cluster_sync_all();  // start: Q is in TMEM, its staging (P, Sx) is free, in both CTAs
       tc_fence_after();
 
-      bool ok = true;
+      bool ok = !aborted();
+      const uint32_t last = n + it.nt - 1;
+      const uint32_t i0 = (n ^ sl) & 1;  // this set's first tile
       if (own) {
         uint64_t rmask = 0;  // the drafts that this row's token sees
         if (R < live_rows) {
@@ -558,38 +605,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           const int64_t nv = min(int64_t(s.nd), p.cap - int64_t(s.pre));
           if (nv < 64) rmask &= (uint64_t(1) << nv) - 1;
         }
-        const float c = sC[R];
         const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
         auto entry_ok = [&](uint32_t i) -> bool {  // entry 32 h + lane of tile i lies in the prefix
-          const uint32_t e = (it.tile0 + i) * kTile + 32 * h + lane;
+          const uint32_t e = (it.tile0 + i) * kTile + kCols * h + lane;
           if (i >= it.nt || e >= s.n_sel) return false;
           return !idx || static_cast<uint32_t>(idx[e]) < s.pre;
         };
-        bool e_ok = entry_ok(0);
-        float ref = -INFINITY, limit = -INFINITY, m6 = INFINITY;
-        uint64_t l2 = 0;  // the row's sum over even and odd columns
+        bool e_ok = entry_ok(i0);
+        float ref = -INFINITY;  // the reference that l2 is relative to
+        uint64_t l2 = 0;        // the row's sum over even and odd columns
         const uint64_t c2 = pack2(c, c);
         const bool arms = h == 0 && (q & 1) == 0 && lane == 0;
         // a wait that ran out ends the loop of both warps of a row at the next vote
-        bool dead = false;
-        for (uint32_t i = 0; i < it.nt; ++i) {
-          const uint32_t m = n + i, sl = m & 1;
-          dead = dead || aborted();
+        bool dead = !ok;
+        for (uint32_t i = i0; i < it.nt; i += 2) {
+          const uint32_t m = n + i, ph = (m >> 1) & 1;
           if (arms) mbar_arrive_expect_tx(&bars[B_SXFULL + sl], kSxBytes);
           uint32_t vis = __ballot_sync(0xffffffffu, e_ok);
-          e_ok = entry_ok(i + 1);
-          const uint32_t e0 = (it.tile0 + i) * kTile + 32 * h;
-          if (e0 + 32 > s.n_sel)  // drafts among the columns
+          e_ok = entry_ok(i + 2);
+          const uint32_t e0 = (it.tile0 + i) * kTile + kCols * h;
+          if (e0 + kCols > s.n_sel)  // drafts among the columns
             vis |= e0 >= s.n_sel ? (e0 - s.n_sel < 64 ? uint32_t(rmask >> (e0 - s.n_sel)) : 0u) : uint32_t(rmask << (s.n_sel - e0));
-          dead = dead || !warp_wait(&bars[B_SFULL + sl], (m >> 1) & 1);
+          dead = dead || !warp_wait(&bars[B_SFULL + sl], ph);
           tc_fence_after();
           uint32_t r[32];
-          tmem_ld32(lane_addr + kColS + kTile * sl + 32 * h, r);
+          tmem_ld32(lane_addr + kColS + kTile * sl + kCols * h, r);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_SFREE + sl]);
-          dead = dead || !warp_wait_cluster(&bars[B_SXFULL + sl], (m >> 1) & 1);
+          dead = dead || !warp_wait_cluster(&bars[B_SXFULL + sl], ph);
           const float4* sx = reinterpret_cast<const float4*>(smem + kOffSx + sl * kSxBytes + 4096 * (2 * (q & 1) + h)) + lane;
           uint64_t z[16];  // logits over c
 #pragma unroll
@@ -618,40 +663,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             }
           }
           mx *= c;
-          float a = 1.0f;
-          const bool moves = pair_any(q, mx > limit || dead);
+          // the reference after the tile before, from the other set
+          float old = -INFINITY;
+          if (i > 0) {
+            dead = dead || !warp_wait(&bars[B_REF + (sl ^ 1)], ((m - 1) >> 1) & 1);
+            old = sRef[64 * (sl ^ 1) + rl];
+          }
+          float to = old, a = 1.0f;
+          const bool moves = pair_any(pair, mx > old + kMoveLog2 || dead);
           // (the vote needs the loaded values, so every lane's loads from the slot have returned)
           if (lane == 0) mbar_arrive_peer_relaxed(peer_smem + kOffBar + 8 * (B_SXFREE + sl));
           if (moves) {  // a reference of these 32 rows moves
-            if (pair_any(q, dead)) {
+            if (pair_any(pair, dead)) {
               dead = true;
               break;
             }
-            sPair[64 * h + rl] = mx;
-            pair_sync(q);
-            mx = fmaxf(mx, sPair[64 * (h ^ 1) + rl]);
-            if (mx > limit) {
-              const float to = mx + kHeadroomLog2;
-              a = ref == -INFINITY ? 0.0f : ex2(ref - to);
-              ref = to;
-              limit = to + kMoveLog2;
-              m6 = to - kPLog2;
-              l2 = fma2(l2, pack2(a, a), 0);
-            }
-            if (i == 0) a = 1.0f;  // (O starts with this tile)
-            if (__any_sync(0xffffffffu, a != 1.0f)) {
-              dead = !warp_wait(&bars[B_VFREE + ((m - 1) & (kStages - 1))], ((m - 1) >> 2) & 1);
-              tc_fence_after();
-              rescale_o(o_addr, a);
+            sPair[64 * (2 * sl + h) + rl] = mx;
+            pair_sync(pair);
+            mx = fmaxf(mx, sPair[64 * (2 * sl + (h ^ 1)) + rl]);
+            if (mx > old + kMoveLog2) {
+              to = mx + kHeadroomLog2;
+              if (i > 0) a = ex2(old - to);  // (O starts with the first tile; no reference so far: 0)
             }
           }
+          if (h == 0) {
+            sRef[64 * sl + rl] = to;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_REF + sl]);
+          }
+          if (to != ref) {
+            const float f = ex2(ref - to);
+            l2 = fma2(l2, pack2(f, f), 0);
+            ref = to;
+          }
+          if (moves && __any_sync(0xffffffffu, a != 1.0f)) {
+            dead = !warp_wait(&bars[B_VFREE + ((m - 1) & (kStages - 1))], ((m - 1) >> 2) & 1);
+            tc_fence_after();
+            rescale_o(o_addr, a);
+          }
           // P's slot is free in both CTAs
-          dead = dead || !warp_wait_cluster(&bars[B_PFREE + sl], ((m >> 1) & 1) ^ 1);
+          dead = dead || !warp_wait_cluster(&bars[B_PFREE + sl], ph ^ 1);
           const uint32_t px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + sl);
           if (h == 0) st_async_f32(peer_smem + kOffAx + 4 * (64 * sl + rl), a, px_bar);
           const uint32_t pw = kOffP + sl * kPBytes + h * (kPBytes / 2) + 32 * q * 64;  // this warp's 2 KiB
           uint8_t* prow = smem + pw + lane * 64;
-          const uint64_t m62 = pack2(-m6, -m6);
+          const float m6 = ref == -INFINITY ? -INFINITY : kPLog2 - ref;
+          const uint64_t m62 = pack2(m6, m6);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t w[4];
@@ -674,83 +731,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           }
         }
         ok = !dead;
-        // the row's sum; reference and sum to both CTAs
+        // the row's sum over its four threads; reference and sum to both CTAs
+        quad_sync(q);
+        const float fin = sRef[64 * (last & 1) + rl];
         float l, l1;
         unpack2(l2, l, l1);
         l += l1;
-        if (h == 1) sPair[128 + rl] = l;
-        pair_sync(q);
-        if (h == 0) {
-          l += sPair[128 + rl];
-          sM[R] = ref;
-          sL[R] = l;
-          st_peer_f32(peer_smem + kOffM + 4 * R, ref);
-          st_peer_f32(peer_smem + kOffL + 4 * R, l);
+        if (l > 0.0f) l *= ex2(ref - fin);
+        if (h4 != 0) sPair[64 * h4 + rl] = l;
+        quad_sync(q);
+        if (h4 == 0) {
+          l += sPair[64 + rl] + sPair[128 + rl] + sPair[192 + rl];
+          sPair[rl] = l;
+          st_peer_f32(peer_smem + kOffMLx + 4 * rl, fin);
+          st_peer_f32(peer_smem + kOffMLx + 4 * (64 + rl), l);
         }
-      } else {
-        // P(j)'s rows from the other CTA have arrived, O's rows follow a moved reference
-        auto take_p = [&](uint32_t m) -> bool {
-          const uint32_t sl = m & 1;
-          if (h == 0 && (q & 1) == 0 && lane == 0) mbar_arrive_expect_tx(&bars[B_PXFULL + sl], kPBytes / 2 + 256);
-          if (!warp_wait_cluster(&bars[B_PXFULL + sl], (m >> 1) & 1)) return false;
-          const float a = sAx[64 * sl + rl];
-          if (__any_sync(0xffffffffu, a != 1.0f)) {
-            if (!warp_wait(&bars[B_VFREE + ((m - 1) & (kStages - 1))], ((m - 1) >> 2) & 1)) return false;
-            tc_fence_after();
-            rescale_o(o_addr, a);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_PREADY + sl]);
-          return true;
-        };
-        for (uint32_t i = 0; i < it.nt && !aborted(); ++i) {
-          const uint32_t m = n + i, sl = m & 1;
-          if (!warp_wait(&bars[B_SFULL + sl], (m >> 1) & 1)) { ok = false; break; }
+      } else if (sl == 0) {
+        // send S's rows over: warps 0-7, every tile
+        for (uint32_t i = 0; ok && i < it.nt; ++i) {
+          const uint32_t m = n + i, to = m & 1, ph = (m >> 1) & 1;
+          ok = warp_wait(&bars[B_SFULL + to], ph);
           tc_fence_after();
           uint32_t r[32];
-          tmem_ld32(lane_addr + kColS + kTile * sl + 32 * h, r);
+          tmem_ld32(lane_addr + kColS + kTile * to + kCols * h, r);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_SFREE + sl]);
+          if (lane == 0) mbar_arrive(&bars[B_SFREE + to]);
           // (the receiver has read S(m - 2): its slot and its staging here are free)
-          if (!warp_wait_cluster(&bars[B_SXFREE + sl], ((m >> 1) & 1) ^ 1)) { ok = false; break; }
-          const uint32_t wo = sl * kSxBytes + 4096 * (2 * (q & 1) + h);
+          ok = ok && warp_wait_cluster(&bars[B_SXFREE + to], ph ^ 1);
+          const uint32_t wo = to * kSxBytes + 4096 * (2 * (q & 1) + h);
           uint4* st = reinterpret_cast<uint4*>(smem + kOffSt + wo) + lane;
 #pragma unroll
           for (int k = 0; k < 8; ++k) st[32 * k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            bulk_peer(peer_smem + kOffSx + wo, smem_u32(smem + kOffSt) + wo, 4096,
-                      peer_smem + kOffBar + 8 * (B_SXFULL + sl));
-          }
-          // (not behind S(m + 2)'s: S(m + 3) is issued after O(m + 1), which waits for this)
-          if (i > 0 && !take_p(m - 1)) { ok = false; break; }
+          if (lane == 0)
+            bulk_peer(peer_smem + kOffSx + wo, smem_u32(smem + kOffSt) + wo, 4096, peer_smem + kOffBar + 8 * (B_SXFULL + to));
         }
-        if (ok) ok = !aborted() && take_p(n + it.nt - 1);
+      } else {
+        // take P's arrival: warps 8-15, every tile; O's rows follow a moved reference
+        const bool arms = h == 0 && (q & 1) == 0 && lane == 0;
+        for (uint32_t i = 0; ok && i < it.nt; ++i) {
+          const uint32_t m = n + i, at = m & 1;
+          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + at], kPBytes / 2 + 256);
+          ok = warp_wait_cluster(&bars[B_PXFULL + at], (m >> 1) & 1);
+          const float a = sAx[64 * at + rl];
+          if (__any_sync(0xffffffffu, a != 1.0f)) {
+            ok = ok && warp_wait(&bars[B_VFREE + ((m - 1) & (kStages - 1))], ((m - 1) >> 2) & 1);
+            tc_fence_after();
+            rescale_o(o_addr, a);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_PREADY + at]);
+        }
       }
-      const uint32_t last = n + it.nt - 1;
       n += it.nt;
-      ok = ok && !aborted();
       if (ok) ok = warp_wait(&bars[B_VFREE + (last & (kStages - 1))], (last >> 2) & 1);
       if (!ok) give_up();
       __syncwarp();
       cluster_sync_all();  // end: O, references and sums are complete in both CTAs
       tc_fence_after();
       // ---- out ----
-      const float l = sL[R], ref = sM[R];
+      const float ref = own ? sRef[64 * (last & 1) + rl] : sMLx[rl], l = own ? sPair[rl] : sMLx[64 + rl];
       const bool whole = it.tile0 == 0 && it.nt == s.tiles;
       const bool live = R < live_rows;
       const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t r[32];
-        tmem_ld32(o_addr + 32 * c, r);
+        tmem_ld32(lane_addr + 64 * h4 + 32 * c, r);
         tmem_ld_wait();
-        const int ch = kHalf * rank + 128 * h + 32 * c;
+        const int ch = kHalf * rank + 64 * h4 + 32 * c;
         if (live && whole) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + R) * kD + ch);
 #pragma unroll
@@ -770,7 +824,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         }
         __syncwarp();
       }
-      if (live && rank == 0 && h == 0) {
+      if (live && rank == 0 && h4 == 0) {
         if (!whole)
           __stcg(reinterpret_cast<float2*>(p.part_ml) + slot * kRows + R, make_float2(ref, l));
         else if (p.lse)
