@@ -180,7 +180,7 @@ TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int 
   L.n_clusters = fp4kv::tree_clusters(B, rows, cap, top_k, sms);
   size_t off = kAlign;  // status header
   L.first_tile = off;
-  off += up(sizeof(int64_t) * (B + 1));
+  off += up(sizeof(uint32_t) * (B + 2));
   L.part_ml = off;
   off += up(sizeof(float) * 2 * L.n_clusters * 128 * 2);
   L.part_o = off;
@@ -708,6 +708,9 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
       !aligned(idx, 4) || !aligned(ws, kAlign))
     return fail(FP4KV_ERR_INVALID_ARG, "misaligned q/packed/scales/out (16 B), tree_mask (8 B) or ws (256 B)");
   const int sms = num_sms();
+  if (fp4kv::tree_tiles(B, int64_t(T) * H, cap, top_k) >= (int64_t(1) << 32))
+    return fail(FP4KV_ERR_UNSUPPORTED, "B=%d sequences of %lld query rows over cap=%lld rows: 2^32 tiles or more", B,
+                (long long)T * H, (long long)cap);
   const TreeLayout L = tree_layout(B, int64_t(T) * H, cap, top_k, sms);
   if (ws_bytes < L.total) return fail(FP4KV_ERR_WORKSPACE_TOO_SMALL, "ws_bytes %zu < %zu", ws_bytes, L.total);
   fp4kv::TreeAttnParams p{};
@@ -729,7 +732,7 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.n_clusters = L.n_clusters;
   p.min_tiles = fp4kv::tree_min_tiles();
-  p.first_tile = reinterpret_cast<int64_t*>(base + L.first_tile);
+  p.first_tile = reinterpret_cast<uint32_t*>(base + L.first_tile);
   p.part_ml = reinterpret_cast<float*>(base + L.part_ml);
   p.part_o = reinterpret_cast<float*>(base + L.part_o);
   p.status = reinterpret_cast<uint32_t*>(base);

@@ -24,7 +24,7 @@
 //  * warps 0-15 own TMEM lane quarter w % 4 (query rows); warps 0-7 work on the even tiles, 8-15 on
 //    the odd ones. Scores: reference and sum in registers (lane = query row, 32 columns a thread);
 //    the reference is handed from set to set. Values: P's arrival, O's rescaling, the output.
-// Numerics: q as fp16 times a power of two per row (exact within 2^29 of the row's maximum), v exact
+// Numerics: q as fp16 times a power of two per row (exact down to 2^-28 of the row's maximum), v exact
 // in fp16, S and O in fp32. The reference m moves only when a logit passes it by 2^9 (log2 domain),
 // to 2^3 above the maximum; p is stored as p * 2^6 in fp16, so the row's largest is at least 2^3 and at
 // most 2^15: 11 bits each, and below 2^-14 a step of 2^-24, 2^-27 of the largest. The sums are fp32.
@@ -55,7 +55,8 @@ constexpr uint32_t kOffV = 0;                     // (scores: first Q's way into
 constexpr uint32_t kOffP = kOffV + kStages * kVBytes;  // 4 slots: as it is made, and as it arrives
 constexpr uint32_t kOffBar = kOffP + kSlots * kPBytes;
 constexpr uint32_t kOffMisc = kOffBar + 320;
-constexpr uint32_t kOffC = kOffBar + 384;         // scores: [128] logit scale (log2 domain) per query row
+constexpr uint32_t kOffIter = kOffBar + 336;      // the cluster's range (a SegIter)
+constexpr uint32_t kOffC = kOffBar + 448;         // scores: [128] power of two of the query rows
 constexpr uint32_t kOffPair = kOffC + 512;        // scores: [4][128] exchange between a row's four threads
 constexpr uint32_t kOffRef = kOffPair + 2048;     // scores: [2][128] reference after the last tile of either parity
 constexpr uint32_t kOffA = kOffRef + 1024;        // values: [4 slots][128] factors of O
@@ -115,6 +116,13 @@ FP4KV_DEV void st_async_f32(uint32_t dst, float v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(dst), "f"(v), "r"(bar) : "memory");
 }
 
+FP4KV_DEV void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {  // 0 bytes: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+FP4KV_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+FP4KV_DEV void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+
 // two fp32 at once
 FP4KV_DEV uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -141,20 +149,25 @@ FP4KV_DEV uint32_t elect_lane() {
 }
 // The MMA and commit wrappers below are called by the whole warp; the lane with `go` issues. The
 // operands stay warp-uniform that way: inside a branch of one lane each MMA took 100 cycles to issue.
+// Descriptors go as their low word (address, leading offset) and a constant high one.
 // D[tmem] (+)= A * B^T, fp16, A from TMEM, B from shared memory
-FP4KV_DEV void umma_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <uint32_t kBHigh>
+FP4KV_DEV void umma_ts(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, g;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 g, %5, 0;\n"
-      " @g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go) : "memory");
+      "{\n .reg .pred p, g;\n .reg .b64 bd;\n mov.b64 bd, {%2, %6};\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 g, %5, 0;\n"
+      " @g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n}"
+      ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go), "n"(kBHigh) : "memory");
 }
 // the same, A from shared memory
-FP4KV_DEV void umma_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <uint32_t kAHigh, uint32_t kBHigh>
+FP4KV_DEV void umma_ss(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, g;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 g, %5, 0;\n"
-      " @g tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go) : "memory");
+      "{\n .reg .pred p, g;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %6};\n mov.b64 bd, {%2, %7};\n setp.ne.b32 p, %4, 0;\n"
+      " setp.ne.b32 g, %5, 0;\n @g tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}"
+      ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go), "n"(kAHigh), "n"(kBHigh) : "memory");
 }
+// High words of the 128-byte and 64-byte swizzled layouts: 1024 or 512 bytes between 8-row groups.
+constexpr uint32_t kHigh128 = (1024u >> 4) | (1u << 14) | (2u << 29), kHigh64 = (512u >> 4) | (1u << 14) | (4u << 29);
 FP4KV_DEV void commit_if(uint32_t go, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred g;\n setp.ne.b32 g, %1, 0;\n"
@@ -199,7 +212,7 @@ struct Seq {
   uint32_t pre;    // rows of the prefix (cap < 2^31)
   uint32_t n_sel;  // entries before the drafts: the prefix, or the selection
   uint32_t tiles, groups;
-  FP4KV_DEV int64_t work() const { return int64_t(tiles) * groups; }
+  FP4KV_DEV uint32_t work() const { return tiles * groups; }
 };
 FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
   Seq s;
@@ -210,32 +223,59 @@ FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
   s.groups = (static_cast<uint32_t>(s.nd) * p.H + kRows - 1) / kRows;
   return s;
 }
-// Clusters in use for `total` tiles: at least min_tiles each.
-FP4KV_DEV int64_t clusters_used(int64_t total, int n_clusters, int min_tiles) {
-  return max(int64_t(1), min(int64_t(n_clusters), (total + min_tiles - 1) / min_tiles));
+// All tile counts fit 32 bits (the host refuses more): a 64-bit division is a call of 100 instructions.
+// Clusters in use for `total` tiles of `items` items, whose tiles are `tiles` each (0: not all the same):
+// at least min_tiles each. Where whole fractions of an item to a cluster cost no more than the parts
+// that begin and end anywhere, they are taken: a cluster then has one segment, not two. A segment
+// costs about as much as 8 tiles (Q, the pipeline's start, the output: 18,000 of 2,300 cycles).
+FP4KV_DEV uint32_t clusters_used(uint32_t total, uint32_t items, uint32_t tiles, uint32_t n_clusters, uint32_t min_tiles) {
+  const uint32_t n = max(1u, min(n_clusters, total / min_tiles + (total % min_tiles != 0)));
+  if (tiles == 0 || items > n) return n;
+  const uint32_t k = n / items;  // clusters an item
+  return (tiles + k - 1) / k <= total / n + 8 ? k * items : n;
+}
+// floor(total * i / used): where cluster i's range starts.
+FP4KV_DEV uint32_t range_start(uint32_t total, uint32_t used, uint32_t i) {
+  const uint32_t per = total / used;
+  return per * i + (total - per * used) * i / used;
+}
+// The cluster of tile x: the largest i whose range starts at x or before.
+FP4KV_DEV uint32_t cluster_of(uint32_t total, uint32_t used, uint32_t x) {
+  uint32_t i = min(used - 1, static_cast<uint32_t>(static_cast<float>(x) / static_cast<float>(total) * static_cast<float>(used)));
+  while (i > 0 && range_start(total, used, i) > x) --i;
+  while (i + 1 < used && range_start(total, used, i + 1) <= x) ++i;
+  return i;
 }
 
 // A cluster's range of tiles, segment by segment (a segment: consecutive tiles of one item).
-struct SegIter {
+struct alignas(16) SegIter {
+  uint32_t off, rem;  // tiles of sequence b already passed; tiles still to do
   int b;
-  int64_t off, rem;  // tiles of sequence b already passed; tiles still to do
-  Seq s;
+  bool ready;         // the segment below is still to be done
   uint32_t g, tile0, nt;
+  Seq s;
+  FP4KV_DEV void cut() {
+    g = off / s.tiles;
+    tile0 = off - g * s.tiles;
+    nt = min(s.tiles - tile0, rem);
+    off += nt;
+    rem -= nt;
+  }
   FP4KV_DEV bool next(const TreeAttnParams& p) {
-    if (rem <= 0) return false;
-    s = seq_of(p, b);
+    if (ready) {
+      ready = false;
+      return true;
+    }
+    if (rem == 0) return false;
     while (off >= s.work()) {
       off -= s.work();
       s = seq_of(p, ++b);
     }
-    g = static_cast<uint32_t>(off / s.tiles);
-    tile0 = static_cast<uint32_t>(off - int64_t(g) * s.tiles);
-    nt = static_cast<uint32_t>(min(int64_t(s.tiles - tile0), rem));
-    off += nt;
-    rem -= nt;
+    cut();
     return true;
   }
 };
+static_assert(sizeof(SegIter) <= 448 - 336 && kOffIter % 16 == 0, "the range's place");
 
 // One thread's share of a tile: chunks j and j + 4 of a row (64 channels each: 32 code bytes, 4 scales).
 struct RawRow {
@@ -291,20 +331,19 @@ FP4KV_DEV void rescale_o(uint32_t addr, float a) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_attn(const TreeAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  float* sC = reinterpret_cast<float*>(smem + kOffC);
+  int* sLow = reinterpret_cast<int*>(smem + kOffC);
   float* sPair = reinterpret_cast<float*>(smem + kOffPair);
   float* sRef = reinterpret_cast<float*>(smem + kOffRef);
   const float* sA = reinterpret_cast<const float*>(smem + kOffA);
   const float* sML = reinterpret_cast<const float*>(smem + kOffML);
-  int64_t* s_off = reinterpret_cast<int64_t*>(smem + kOffMisc);  // the range's start: tiles into sequence s_b
-  int64_t* s_rem = s_off + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 16);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = s_tmem + 1;
-  int* s_b = reinterpret_cast<int*>(s_tmem + 2);
+  SegIter* s_it = reinterpret_cast<SegIter*>(smem + kOffIter);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool values = cluster_ctarank() != 0;  // the CTA that makes O
-  const int cl = blockIdx.x >> 1;
+  const uint32_t cl = blockIdx.x >> 1;
+  griddep_launch_dependents();  // (k_tree_merge, which waits for this grid before it reads anything)
   griddep_wait();
 
   // the smem alignment that the swizzled operands need (the same in both CTAs of a launch)
@@ -312,49 +351,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     if (tid == 0) atomicOr(p.status, 2u);
     return;
   }
-  // ---- this cluster's range of tiles ----
+  // ---- this cluster's range of tiles, and its first segment ----
+  if (warp == kMmaWarp) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
   if (warp == 0) {
-    int64_t total = 0;
-    for (int b = lane; b < p.B; b += 32) {
+    Seq mine{};  // of sequence lane, then of the 32 at hand
+    if (lane < p.B) mine = seq_of(p, lane);
+    uint32_t total = mine.work(), items = mine.groups;
+    uint32_t most = mine.work() ? mine.tiles : 0, least = mine.work() ? mine.tiles : 0xffffffffu;
+#pragma unroll 1
+    for (int b = lane + 32; b < p.B; b += 32) {
       const Seq s = seq_of(p, b);
       total += s.work();
+      items += s.groups;
+      if (s.work()) {
+        most = max(most, s.tiles);
+        least = min(least, s.tiles);
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t used = clusters_used(total, p.n_clusters, p.min_tiles);
-    const int64_t x0 = cl < used ? total * cl / used : total;
-    const int64_t x1 = cl < used ? total * (cl + 1) / used : total;
+    total = __reduce_add_sync(0xffffffffu, total);
+    items = __reduce_add_sync(0xffffffffu, items);
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    const uint32_t used = clusters_used(total, items, most == least ? most : 0, p.n_clusters, p.min_tiles);
+    const uint32_t x0 = cl < used ? range_start(total, used, cl) : total;
+    const uint32_t x1 = cl < used ? range_start(total, used, cl + 1) : total;
     // where x0 lies, and (cluster 0) each sequence's first tile for the merge
-    int64_t at = 0;
+    uint32_t at = 0;
     bool found = x1 <= x0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B && (!found || cl == 0); b0 += 32) {
       const int b = b0 + lane;
-      int64_t n = 0;
-      if (b < p.B) {
-        const Seq s = seq_of(p, b);
-        n = s.work();
+      if (b0 > 0) {
+        mine = Seq{};
+        if (b < p.B) mine = seq_of(p, b);
       }
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t n = mine.work();
+      uint32_t incl = n;
+#pragma unroll 1
+      for (int o = 1; o < 32 && o < p.B; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       if (cl == 0 && !values && b < p.B) p.first_tile[b] = at + incl - n;
       const uint32_t hit = __ballot_sync(0xffffffffu, at + incl > x0);
       if (!found && hit) {
         if (lane == __ffs(hit) - 1) {
-          *s_b = b;
-          *s_off = x0 - (at + incl - n);
+          SegIter first;
+          first.b = b;
+          first.off = x0 - (at + incl - n);
+          first.rem = x1 - x0;
+          first.s = mine;
+          first.cut();
+          first.ready = true;
+          *s_it = first;
         }
         found = true;
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      *s_rem = x1 - x0;
+      if (x1 <= x0) s_it->ready = false;
       *s_abort = 0;
-      if (cl == 0 && !values) p.first_tile[p.B] = total;
+      if (cl == 0 && !values) {
+        p.first_tile[p.B] = total;
+        p.first_tile[p.B + 1] = used;
+      }
     }
   }
   if (tid == 32) {
@@ -376,19 +441,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     fence_mbar_init();
   }
   __syncthreads();
-  if (*s_rem <= 0) return;  // (both CTAs of the cluster)
-  if (warp == kMmaWarp) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
+  SegIter it = *s_it;
+  if (!it.ready) {  // nothing to do, for both CTAs of the cluster
+    if (warp == kMmaWarp) tmem_dealloc(*s_tmem, 512);
+    return;
   }
-  tc_fence_before();
-  cluster_sync_all();  // (the other CTA's barriers exist)
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;
-  SegIter it;
-  it.b = *s_b;
-  it.off = *s_off;
-  it.rem = *s_rem;
+  cluster_arrive_relaxed();  // (the barriers' initialisation has been released by its own fence)
+  // Each role waits where it first needs the other CTA's barriers or TMEM; its first loads come before.
+  uint32_t tmem = 0;
+  auto join = [&]() {
+    cluster_wait();
+    tc_fence_after();
+    tmem = *s_tmem;
+  };
   uint32_t n = 0;    // tiles so far, over all segments: slot n % 4
   uint32_t seg = 0;  // segments so far
 
@@ -419,26 +484,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       const Seq& s = it.s;
       // a drafted row that no token sees counts as absent
       uint64_t seen = 0;
-      for (int t = lane; t < s.nd; t += 32) seen |= p.tree_mask[int64_t(it.b) * p.T + t];
-      seen = uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen))) |
-             (uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen >> 32))) << 32);
+      {
+        const uint64_t* tm = p.tree_mask + int64_t(it.b) * p.T;
+        if (lane < s.nd) seen = tm[lane];
+        if (lane + 32 < s.nd) seen |= tm[lane + 32];
+      }
       const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
       const uint8_t* packed = p.packed + int64_t(it.b) * p.cap * (kD / 2) + 32 * j;
       const uint8_t* scales = p.scales + int64_t(it.b) * p.cap * (kD / kGroup) + 4 * j;
-      // this thread's row of tile i: a position, which is checked only when it is used (it may still be
-      // on its way from the selection)
-      auto pos_of = [&](uint32_t i) -> int32_t {
+      // This thread's row of tile i: the entry, which is turned into a position only when it is used (it may
+      // still be on its way from the selection).
+      auto entry = [&](uint32_t i) -> int32_t {
         const uint32_t e = (it.tile0 + i) * kTile + row;
-        if (i >= it.nt) return -1;
-        if (e < s.n_sel) return idx ? idx[e] : static_cast<int32_t>(e);
-        const uint32_t d = e - s.n_sel;
-        return d < uint32_t(s.nd) && ((seen >> d) & 1) && int64_t(s.pre) + d < p.cap ? static_cast<int32_t>(s.pre + d) : -1;
+        return i < it.nt && idx && e < s.n_sel ? idx[e] : static_cast<int32_t>(e);
       };
-      auto load = [&](RawRow& r, uint32_t i, int32_t pos) {
-        const bool sel = (it.tile0 + i) * kTile + row < s.n_sel;
-        if (static_cast<uint32_t>(pos) < (sel ? s.pre : 0x80000000u)) {
-          const uint8_t* c = packed + int64_t(pos) * (kD / 2);
-          const uint8_t* f = scales + int64_t(pos) * (kD / kGroup);
+      auto load = [&](RawRow& r, uint32_t i, int32_t ent) {
+        const uint32_t e = (it.tile0 + i) * kTile + row;
+        int64_t pos = static_cast<uint32_t>(ent);
+        bool there = i < it.nt;
+        if (e < s.n_sel) {
+          there = there && static_cast<uint32_t>(ent) < s.pre;
+        } else {
+          const uint32_t d = e - s.n_sel;
+          pos = int64_t(s.pre) + d;
+          there = there && d < uint32_t(s.nd) && ((seen >> d) & 1) && pos < p.cap;
+        }
+        if (there) {
+          const uint8_t* c = packed + pos * (kD / 2);
+          const uint8_t* f = scales + pos * (kD / kGroup);
           ld_nc_32b(r.c[0], c, al32);
           ld_nc_32b(r.c[1], c + 128, al32);
           r.s[0] = *reinterpret_cast<const uint32_t*>(f);
@@ -449,10 +522,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           r.s[0] = r.s[1] = 0;
         }
       };
+      const int32_t e0 = entry(0), e1 = entry(1);
+      int32_t ent = entry(2);
+      seen = uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen))) |
+             (uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen >> 32))) << 32);
       RawRow ra, rb;  // tiles i and i + 1 (each reloaded in place: a copy would wait for its loads)
-      load(ra, 0, pos_of(0));
-      load(rb, 1, pos_of(1));
-      int32_t pos = pos_of(2);
+      load(ra, 0, e0);
+      load(rb, 1, e1);
+      if (seg == 0) join();
       if (!values) ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);  // (Q came through the stages)
       auto tile = [&](RawRow& r, uint32_t i) {
         if (!ok || i >= it.nt) return;
@@ -465,8 +542,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_VFULL + 2 * st + half]);
-        load(r, i + 2, pos);
-        pos = pos_of(i + 3);
+        load(r, i + 2, ent);
+        ent = entry(i + 3);
         next_stage();
       };
       for (uint32_t i = 0; ok && i < it.nt; i += 2) {
@@ -479,6 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   } else if (warp >= kMmaWarp) {
     // ------------------------------ MMA issue (one warp; its warpgroup's others idle) ------------------------------
     fewer_registers<56>();
+    join();
     if (warp == kMmaWarp) {
       const uint32_t go = elect_lane();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -486,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       while (ok && it.next(p)) {
         if (!values) {
           constexpr uint32_t kIdesc = umma_idesc(0u, kRows, kTile, 0u, 0u);
-          const uint64_t dv = sw128_kmajor_desc(smem_u32(smem + kOffV));
+          const uint32_t dv = static_cast<uint32_t>(sw128_kmajor_desc(smem_u32(smem + kOffV)));
           ok = warp_wait(&bars[B_QREADY], seg & 1);
           for (uint32_t i = 0; ok && i < it.nt; ++i) {
             const uint32_t m = n + i, sl = m & (kSlots - 1);
@@ -494,13 +572,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
                  warp_wait(&bars[B_VFULL + 2 * st + 1], sph);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t b0 = dv + ((st * kVBytes) >> 4);
+            const uint32_t b0 = dv + ((st * kVBytes) >> 4);
             const uint32_t d = tm + kColS + kTile * sl;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                umma_ts(go, d, tm + 32 * c + 8 * k, b0 + ((c * kVChunk) >> 4) + 2 * k, kIdesc, (c | k) != 0);
+                umma_ts<kHigh128>(go, d, tm + 32 * c + 8 * k, b0 + ((c * kVChunk) >> 4) + 2 * k, kIdesc, (c | k) != 0);
             commit_if(go, &bars[B_SFULL + sl]);
             commit_if(go, &bars[B_VFREE + 2 * st]);
             commit_if(go, &bars[B_VFREE + 2 * st + 1]);
@@ -509,8 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           }
         } else {
           constexpr uint32_t kIdesc = umma_idesc(0u, kRows, 256, 0u, 1u);
-          const uint64_t dv = sw128_mnmajor_desc(smem_u32(smem + kOffV), kVChunk);
-          const uint64_t dp = sw64_kmajor_desc(smem_u32(smem + kOffP));
+          const uint32_t dv = static_cast<uint32_t>(sw128_mnmajor_desc(smem_u32(smem + kOffV), kVChunk));
+          const uint32_t dp = static_cast<uint32_t>(sw64_kmajor_desc(smem_u32(smem + kOffP)));
           for (uint32_t i = 0; ok && i < it.nt; ++i) {
             const uint32_t m = n + i, sl = m & (kSlots - 1);
             ok = warp_wait(&bars[B_PREADY + sl], (m >> 2) & 1);
@@ -519,13 +597,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
               ok = ok && warp_wait(&bars[B_VFULL + 2 * st + hf], sph);
               if (ok) {
                 tc_fence_after();
-                const uint64_t a0 = dp + ((sl * kPBytes + hf * (kPBytes / 2)) >> 4);
-                const uint64_t b0 = dv + ((st * kVBytes + hf * 4096) >> 4);
+                const uint32_t a0 = dp + ((sl * kPBytes + hf * (kPBytes / 2)) >> 4);
+                const uint32_t b0 = dv + ((st * kVBytes + hf * 4096) >> 4);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                   for (int c = 0; c < 2; ++c)
-                    umma_ss(go, tm + 256 * c, a0 + 2 * k, b0 + ((2048 * k + 4 * c * kVChunk) >> 4), kIdesc, i > 0 || (hf | k) != 0);
+                    umma_ss<kHigh64, kHigh128>(go, tm + 256 * c, a0 + 2 * k, b0 + ((2048 * k + 4 * c * kVChunk) >> 4), kIdesc, i > 0 || (hf | k) != 0);
                 commit_if(go, &bars[B_VFREE + 2 * st + hf]);
               }
             }
@@ -544,11 +622,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       if (!warp_wait(&bars[B_DONE], 0)) give_up();
     }
   } else {
+    more_registers<72>();  // (as launched: said so, the allocator spills less)
     const int q = warp & 3, h4 = warp >> 2, h = h4 & 1;
     const uint32_t set = warp >> 3;
     const int pair = 4 * static_cast<int>(set) + q;
     const int R = 32 * q + lane;  // query row of the item
-    const uint32_t lane_addr = tmem + (uint32_t(32 * q) << 16);
+    uint32_t lane_addr = 0;
     const uint32_t peer_smem = map_peer(smem_u32(smem), values ? 0 : 1);
     while (it.next(p)) {
       const Seq& s = it.s;
@@ -559,45 +638,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       bool ok = !aborted();
       if (!values) {
         // ------------------------------ scores and softmax ------------------------------
-        // ---- Q: bf16 -> fp16 times a power of two, through shared memory into TMEM ----
+        // ---- Q: bf16 -> fp16 times a power of two, in shared memory, then into TMEM ----
         // (the last item's products are complete: its stages and Q's place are free)
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint4 v[4][2];
+        for (int r = warp; r < kRows; r += kSoftWarps) {
+          const uint16_t* src = p.q + (row0 + (r < live_rows ? r : 0)) * kD + 8 * lane;
+          const uint32_t dst = smem_u32(smem) + kOffV + r * 1024 + ((lane ^ (r & 7)) << 4);
+          cp_async_16(dst, src, r < live_rows ? 16 : 0);
+          cp_async_16(dst + 512, src + kD / 2, r < live_rows ? 16 : 0);
+        }
+        uint64_t rmask = 0;  // the drafts that this row's token sees
+        if (R < live_rows) {
+          rmask = p.tree_mask[int64_t(it.b) * p.T + (it.g * kRows + R) / uint32_t(p.H)];
+          const int64_t nv = min(int64_t(s.nd), p.cap - int64_t(s.pre));
+          if (nv < 64) rmask &= (uint64_t(1) << nv) - 1;
+        }
+        if (seg == 0) {
+          join();
+          lane_addr = tmem + (uint32_t(32 * q) << 16);
+        }
+        cp_async_wait_all();
+        // (a negative scale goes into q's sign: the factor of the logits is positive)
+        const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll 1
+        for (int r = warp; r < kRows; r += kSoftWarps) {  // (each lane what it has copied itself)
+          uint8_t* at = smem + kOffV + r * 1024 + ((lane ^ (r & 7)) << 4);
+          const uint4 v0 = *reinterpret_cast<const uint4*>(at), v1 = *reinterpret_cast<const uint4*>(at + 512);
+          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+          uint32_t m2 = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = warp + kSoftWarps * (4 * part + k);
-            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-            if (r < live_rows) {
-              const uint16_t* src = p.q + (row0 + r) * kD + 8 * lane;
-              v[k][0] = *reinterpret_cast<const uint4*>(src);
-              v[k][1] = *reinterpret_cast<const uint4*>(src + kD / 2);
-            }
-          }
+          for (int u = 0; u < 8; ++u) m2 = __vmaxu2(m2, w[u] & 0x7fff7fffu);
+          const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+          // The power of two that brings the row's maximum into [2^14, 2^15), whose fp16 exponent is 29:
+          // an exponent field x of bf16 becomes x - low (values of field low or less, below 2^-28 of the
+          // maximum, come out wrong by up to 2^-29 of it).
+          const int low = max(int(m >> 7), 29) - 29;
+          const uint32_t low2 = static_cast<uint32_t>(low) * 0x00800080u;
+          uint32_t f[8];  // (field and mantissa three bits up, the sign beside them)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = warp + kSoftWarps * (4 * part + k);
-            const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-            uint32_t m2 = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) m2 = __vmaxu2(m2, w[u] & 0x7fff7fffu);
-            const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-            int e = 0;  // the power of two that brings the row's maximum into [2^14, 2^15)
-            if (m != 0) e = max(-126, min(127, 14 - max(-126, int(m >> 7) - 127)));
-            // (a negative scale goes into q's sign: the factor of the logits is positive)
-            const float up = copysignf(__uint_as_float(uint32_t(127 + e) << 23), p.sm_scale);
-            uint32_t f[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              f[u] = pack_f16x2(__uint_as_float(w[u] << 16) * up, __uint_as_float(w[u] & 0xffff0000u) * up);
-            uint8_t* dst = smem + kOffV + r * 1024;
-            *reinterpret_cast<uint4*>(dst + ((lane ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(dst + 512 + ((lane ^ (r & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
-            if (lane == 0)
-              sC[r] = fmaxf(fabsf(p.sm_scale) * kLog2e * __uint_as_float(uint32_t(127 - e / 2) << 23) *
-                                __uint_as_float(uint32_t(127 - (e - e / 2)) << 23),
-                            2e-38f);  // (above zero: a masked -inf stays -inf)
-          }
+          for (int u = 0; u < 8; ++u)
+            f[u] = ((__vmaxu2(w[u] & 0x7fff7fffu, low2) - low2) << 3) | ((w[u] ^ flip) & 0x80008000u);
+          *reinterpret_cast<uint4*>(at) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(at + 512) = make_uint4(f[4], f[5], f[6], f[7]);
+          if (lane == 0) sLow[r] = low;
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 #pragma unroll 1
@@ -611,18 +694,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           tmem_st16(lane_addr + 64 * h4 + 16 * c, w);
         }
         tmem_st_wait();
-        const float c = sC[R];
+        // q = fp16 * 2^(low - 112)
+        const int up = sLow[R] - 112;
+        const float c = fmaxf(fabsf(p.sm_scale) * kLog2e * __uint_as_float(uint32_t(127 + up / 2) << 23) *
+                                  __uint_as_float(uint32_t(127 + (up - up / 2)) << 23),
+                              2e-38f);  // (above zero: a masked -inf stays -inf)
         // the same bytes are written by the dequantizing warps next and read by the tensor cores
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_QREADY]);
 
-        uint64_t rmask = 0;  // the drafts that this row's token sees
-        if (R < live_rows) {
-          rmask = p.tree_mask[int64_t(it.b) * p.T + (it.g * kRows + R) / uint32_t(p.H)];
-          const int64_t nv = min(int64_t(s.nd), p.cap - int64_t(s.pre));
-          if (nv < 64) rmask &= (uint64_t(1) << nv) - 1;
-        }
         const int32_t* idx = p.idx ? p.idx + int64_t(it.b) * p.top_k : nullptr;
         auto entry_ok = [&](uint32_t i) -> bool {  // entry 32 h + lane of tile i lies in the prefix
           const uint32_t e = (it.tile0 + i) * kTile + kCols * h + lane;
@@ -734,6 +815,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         quad_sync(q);  // (the sums have been read)
       } else {
         // ------------------------------ O: arrivals, rescaling ------------------------------
+        if (seg == 0) {
+          join();
+          lane_addr = tmem + (uint32_t(32 * q) << 16);
+        }
         const bool arms = h == 0 && q == 0 && lane == 0;
         for (uint32_t i = i0; ok && i < it.nt; i += 2) {
           const uint32_t m = n + i, sl = m & (kSlots - 1);
@@ -819,53 +904,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
 }
 
 // Joins the parts of items that several clusters worked on: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-// A block takes 32 query rows and 64 channels: lanes along the rows as the parts lie, then through shared
+// A block takes 32 query rows and 128 channels: lanes along the rows as the parts lie, then through shared
 // memory to lanes along the channels.
-constexpr int kMergeCh = 64;
+constexpr int kMergeCh = 128;
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
   griddep_wait();
   __shared__ float tile[32][kMergeCh + 1];
   const int blocks = (p.T * p.H + 31) / 32;
   const int b = blockIdx.x / blocks, r0 = 32 * (blockIdx.x % blocks), ch0 = kMergeCh * blockIdx.y;
+  const uint32_t total = p.first_tile[p.B], used = p.first_tile[p.B + 1], first = p.first_tile[b];
   const Seq s = seq_of(p, b);
   const int n_rows = s.nd * p.H;
   if (r0 >= n_rows) return;
-  const int64_t total = p.first_tile[p.B], used = clusters_used(total, p.n_clusters, p.min_tiles);
-  const int64_t x = p.first_tile[b] + int64_t(r0 / kRows) * s.tiles;
-  // the cluster of tile x: the largest i with floor(total i / used) <= x
-  const int64_t c0 = ((x + 1) * used - 1) / total, c1 = ((x + s.tiles) * used - 1) / total;
+  const uint32_t x = first + (r0 / kRows) * s.tiles;
+  const uint32_t c0 = cluster_of(total, used, x), c1 = cluster_of(total, used, x + s.tiles - 1);
   if (c0 == c1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = r0 % kRows + lane, n = static_cast<int>(c1 - c0 + 1);
   const bool live = r0 + lane < n_rows;
-  auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  const float4* po = reinterpret_cast<const float4*>(p.part_o);
-  float m = -INFINITY;
+  auto slot = [&](int i) { return int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)); };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + R;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (ch0 / 4 + warp) * kRows + R;
+  float m = -INFINITY, l = 0.0f;
+  float4 o[4] = {};  // fours warp, warp + 8, ... of the block's channels
   if (live) {
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
-      const float2 v = __ldcg(ml + slot(i) * kRows + R);
-      if (v.y > 0.0f) m = fmaxf(m, v.x);
-    }
-  }
-  float l = 0.0f;
-  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};  // fours warp and warp + 8 of the block's
-  if (live) {
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float2 v = __ldcg(ml + slot(i) * kRows + R);
-      const float4* src = po + (slot(i) * (kD / 4) + ch0 / 4 + warp) * kRows + R;
-      const float4 f0 = __ldcg(src), f1 = __ldcg(src + 8 * kRows);
-      const float w = v.y > 0.0f ? ex2(v.x - m) : 0.0f;
-      l = fmaf(w, v.y, l);
-      o[0].x = fmaf(w, f0.x, o[0].x); o[0].y = fmaf(w, f0.y, o[0].y); o[0].z = fmaf(w, f0.z, o[0].z); o[0].w = fmaf(w, f0.w, o[0].w);
-      o[1].x = fmaf(w, f1.x, o[1].x); o[1].y = fmaf(w, f1.y, o[1].y); o[1].z = fmaf(w, f1.z, o[1].z); o[1].w = fmaf(w, f1.w, o[1].w);
+      const float2 v = __ldcg(ml + slot(i) * kRows);
+      float4 f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = __ldcg(po + slot(i) * (kD / 4) * kRows + 8 * k * kRows);
+      const float to = v.y > 0.0f ? fmaxf(m, v.x) : m;
+      const float w0 = m == to ? 1.0f : ex2(m - to), w1 = v.y > 0.0f ? ex2(v.x - to) : 0.0f;
+      m = to;
+      l = fmaf(w1, v.y, l * w0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k].x = fmaf(w1, f[k].x, o[k].x * w0);
+        o[k].y = fmaf(w1, f[k].y, o[k].y * w0);
+        o[k].z = fmaf(w1, f[k].z, o[k].z * w0);
+        o[k].w = fmaf(w1, f[k].w, o[k].w * w0);
+      }
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 4; ++k) {
     float* t = &tile[lane][4 * (warp + 8 * k)];
     t[0] = o[k].x * inv; t[1] = o[k].y * inv; t[2] = o[k].z * inv; t[3] = o[k].w * inv;
   }
@@ -876,9 +960,11 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
   for (int k = 0; k < 4; ++k) {
     const int r = warp + 8 * k;
     if (r0 + r >= n_rows) continue;
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(tile[r][2 * lane + 1]), "f"(tile[r][2 * lane]));
-    *reinterpret_cast<uint32_t*>(p.out + (row0 + r) * kD + ch0 + 2 * lane) = w;
+    uint2 w;
+    const float* t = &tile[r][4 * lane];
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(t[1]), "f"(t[0]));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(t[3]), "f"(t[2]));
+    *reinterpret_cast<uint2*>(p.out + (row0 + r) * kD + ch0 + 4 * lane) = w;
   }
 }
 
@@ -886,9 +972,12 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
 
 int tree_min_tiles() { return 2; }
 
+int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k) {
+  return B * ((rows + kRows - 1) / kRows) * (((top_k ? top_k : cap) + 64 + kTile - 1) / kTile);
+}
+
 int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms) {
-  const int64_t tiles = ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile;
-  const int64_t total = B * ((rows + kRows - 1) / kRows) * tiles;
+  const int64_t total = tree_tiles(B, rows, cap, top_k);
   const int64_t most = (total + tree_min_tiles() - 1) / tree_min_tiles();
   return static_cast<int>(most < num_sms / 2 ? most : num_sms / 2);
 }

@@ -310,7 +310,8 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  * and outputs of the others are not touched, and mask bits at or above it are ignored. Prefix
  * lengths are clamped to [0, cap]; drafted rows at or behind cap are absent. A token that sees
  * nothing gets out = 0, lse = -inf. A row that no token sees is not read.
- * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without. ws: at least
+ * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without;
+ * B * ceil(T H / 128) * ceil((R + 64) / 64) < 2^32 with R = top_k or cap. ws: at least
  * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,
  * initialised once. q, packed, scales and out 16-byte aligned. */
 fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int32_t H, int32_t d,

@@ -195,7 +195,7 @@ def test_dequant_refusals(change, status, word):
     (dict(top_k=(1 << 20) + 1), 2, "top_k"), (dict(idx=None), 2, "top_k"), (dict(cap=0), 2, "cap=0"),
     (dict(cap=1 << 31), 2, "cap"), (dict(q=None), 1, "null"), (dict(mask=None), 1, "null"), (dict(ws=None), 1, "null"),
     (dict(out=FAKE + 8), 1, "misaligned"), (dict(ws=FAKE + 16), 1, "misaligned"), (dict(mask=FAKE + 4), 1, "misaligned"),
-    (dict(wsb=255), 4, "ws_bytes"),
+    (dict(wsb=255), 4, "ws_bytes"), (dict(B=65535, T=64, H=128, idx=None, top_k=0, cap=(1 << 31) - 8), 2, "tiles"),
 ])
 def test_tree_refusals(change, status, word):
     a = dict(q=FAKE, B=2, T=5, H=64, d=512, packed=FAKE, scales=FAKE, cap=100, lens=FAKE, nd=None, mask=FAKE, idx=FAKE,
