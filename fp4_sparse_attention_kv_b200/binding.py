@@ -350,25 +350,38 @@ def swa_quant_fp8(x: torch.Tensor, out: torch.Tensor, dst_row: torch.Tensor | No
                                      _stream(x.device)))
 
 
+# The calls below check and marshal with as few Python operations as they can: for one token the
+# kernel takes less time than a careless check of ten tensors.
+_raw_stream, _raw_device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _call(fn, dev, *args):
-    """A library call with dev as the current device, on dev's current stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    """A library call with device `dev` (its index) current, on dev's current stream."""
+    if dev == _raw_device():
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            st = fn(*args, _raw_stream(dev))
+    if st:
+        _check(st)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows_of(packed, scales, d, dev):
-    """Rows of a cache given as contiguous uint8 planes [..., d/2] and [..., d/16]."""
-    _need(packed, torch.uint8, "packed", dev)
-    _need(scales, torch.uint8, "scales", dev)
-    cap = packed.numel() // (d // 2)
-    if packed.numel() != cap * (d // 2) or scales.numel() != cap * (d // 16):
+def _take(t, dtype, name, dev):
+    """_need for a contiguous tensor on the device of index dev, its address."""
+    if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _need(t, dtype, name, torch.device("cuda", dev))
+    return t.data_ptr()
+
+
+def _cache_rows(packed, scales, d):
+    """Rows of a cache given as planes [..., d/2] and [..., d/16]."""
+    n, m = packed.numel(), scales.numel()
+    cap = 2 * n // d
+    if 2 * n != cap * d or 16 * m != cap * d:
         raise ValueError("packed / scales do not match d")
     return cap
 
@@ -385,55 +398,64 @@ def qkv_norm_rope_fp4(q, kv, *, positions=None, cos_sin=None, rope_dim=0, rope_h
     one = kv if q is None else q
     if one is None:
         raise ValueError("q or kv is required")
-    dev, n, d = one.device, one.shape[0], one.shape[-1]
-    for t, name, dim in ((q, "q", 3), (kv, "kv", 2)):
-        if t is not None:
-            _need(t, torch.bfloat16, name, dev, contiguous=False)
-            if t.dim() != dim or t.shape[0] != n or t.shape[-1] != d or (t.stride(-1) != 1 and t.numel()):
-                raise ValueError("q [n, H, d] and kv [n, d] with unit channel stride expected")
-    H = 0 if q is None else q.shape[1]
-    for t, name in ((q_weight, "q_weight"), (kv_weight, "kv_weight")):
-        if t is not None:
-            _need(t, torch.bfloat16, name, dev)
-            if t.numel() != d:
-                raise ValueError(f"{name}: expected d = {d} values")
-    max_pos = 0
+    dev, n, d = one.get_device(), one.shape[0], one.shape[-1]
+    if dev < 0:
+        raise TypeError("q / kv: expected CUDA tensors")
+    bf16 = torch.bfloat16
+    H = qts = qhs = kvs = 0
+    q_at = kv_at = None
+    if q is not None:
+        if q.dtype is not bf16 or q.dim() != 3 or (q.stride(2) != 1 and q.numel()):
+            raise TypeError("q: expected a bf16 [n, H, d] tensor with unit channel stride")
+        H = q.shape[1]
+        q_at, qts, qhs = q.data_ptr(), _stride(q, 0, H * d), _stride(q, 1, d)
+    if kv is not None:
+        if kv.dtype is not bf16 or kv.dim() != 2 or (kv.stride(1) != 1 and kv.numel()):
+            raise TypeError("kv: expected a bf16 [n, d] tensor with unit channel stride")
+        if kv.shape[0] != n or kv.shape[1] != d or kv.get_device() != dev:
+            raise ValueError("q [n, H, d] and kv [n, d] on one device expected")
+        kv_at, kvs = kv.data_ptr(), _stride(kv, 0, d)
+    qw_at = kw_at = pos_at = cs_at = qo_at = ko_at = dst_at = packed_at = scales_at = None
+    if q_weight is not None:
+        qw_at = _take(q_weight, bf16, "q_weight", dev)
+        if q_weight.numel() != d:
+            raise ValueError(f"q_weight: expected d = {d} values")
+    if kv_weight is not None:
+        kw_at = _take(kv_weight, bf16, "kv_weight", dev)
+        if kv_weight.numel() != d:
+            raise ValueError(f"kv_weight: expected d = {d} values")
+    max_pos = cap = 0
     if rope_dim:
-        _need(positions, torch.int64, "positions", dev)
-        _need(cos_sin, torch.float32, "cos_sin", dev)
+        pos_at, cs_at = _take(positions, torch.int64, "positions", dev), _take(cos_sin, torch.float32, "cos_sin", dev)
         if positions.numel() != n or cos_sin.dim() != 2 or cos_sin.shape[1] != rope_dim:
             raise ValueError("positions [n] and cos_sin [max_pos, rope_dim] expected")
         max_pos = cos_sin.shape[0]
     if q is not None:
         if q_out is None:
-            q_out = torch.empty((n, H, d), dtype=torch.bfloat16, device=dev)
-        _need(q_out, torch.bfloat16, "q_out", dev)
+            q_out = torch.empty((n, H, d), dtype=bf16, device=one.device)
+        qo_at = _take(q_out, bf16, "q_out", dev)
         if q_out.numel() != n * H * d:
             raise ValueError("q_out: expected [n, H, d]")
-    cap = 0
     if kv is None:
         if packed is not None or scales is not None or kv_out is not None:
             raise ValueError("packed, scales and kv_out need kv")
     else:
         if packed is not None or scales is not None:
-            cap = _rows_of(packed, scales, d, dev)
+            packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
+            cap = _cache_rows(packed, scales, d)
             if dst_row is not None:
-                _need(dst_row, torch.int64, "dst_row", dev)
+                dst_at = _take(dst_row, torch.int64, "dst_row", dev)
                 if dst_row.numel() != n:
                     raise ValueError("dst_row: expected [n]")
         elif kv_out is None:
-            kv_out = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+            kv_out = torch.empty((n, d), dtype=bf16, device=one.device)
         if kv_out is not None:
-            _need(kv_out, torch.bfloat16, "kv_out", dev)
+            ko_at = _take(kv_out, bf16, "kv_out", dev)
             if kv_out.numel() != n * d:
                 raise ValueError("kv_out: expected [n, d]")
-    if n == 0:
-        return q_out, kv_out
-    _call(lib().fp4kv_qkv_norm_rope_fp4, dev, _addr(q), 0 if q is None else _stride(q, 0, H * d),
-          0 if q is None else _stride(q, 1, d), H, _addr(q_weight), _addr(q_out) if q is not None else None, _addr(kv),
-          0 if kv is None else _stride(kv, 0, d), _addr(kv_weight), _addr(kv_out), _addr(dst_row), _addr(packed),
-          _addr(scales), cap, n, d, rope_dim, 1 if rope_half else 0, _addr(positions) if rope_dim else None,
-          _addr(cos_sin) if rope_dim else None, max_pos, eps)
+    if n:
+        _call((_lib or lib()).fp4kv_qkv_norm_rope_fp4, dev, q_at, qts, qhs, H, qw_at, qo_at, kv_at, kvs, kw_at, ko_at, dst_at,
+              packed_at, scales_at, cap, n, d, rope_dim, 1 if rope_half else 0, pos_at, cs_at, max_pos, eps)
     return q_out, kv_out
 
 
@@ -446,23 +468,25 @@ def kv_dequant_fp4(packed, scales, src_row=None, out=None, dtype=torch.bfloat16)
     """Rows of the FP4 cache packed [..., d/2], scales [..., d/16] as bf16 or fp32 (out's type,
     else dtype): row src_row[i] (int64 [n]; rows outside the cache give zeros), or every row in
     order. Exact. out [n, d] may have a row stride above d. Returns out."""
-    _need(packed, torch.uint8, "packed")
-    dev, d = packed.device, 2 * packed.shape[-1]
-    cap = _rows_of(packed, scales, d, dev)
-    n = cap
+    dev, d = packed.get_device(), 2 * packed.shape[-1]
+    if dev < 0:
+        raise TypeError("packed: expected a CUDA tensor")
+    packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
+    n = cap = _cache_rows(packed, scales, d)
+    src_at = None
     if src_row is not None:
-        _need(src_row, torch.int64, "src_row", dev)
+        src_at = _take(src_row, torch.int64, "src_row", dev)
         n = src_row.numel()
     if out is None:
-        out = torch.empty((n, d), dtype=dtype, device=dev)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+        out = torch.empty((n, d), dtype=dtype, device=packed.device)
+    f32 = out.dtype is torch.float32
+    if not f32 and out.dtype is not torch.bfloat16:
         raise TypeError(f"out: expected bf16 or fp32, got {out.dtype}")
-    _need(out, out.dtype, "out", dev, contiguous=False)
-    if out.dim() != 2 or out.shape[0] != n or out.shape[1] != d or (out.stride(1) != 1 and out.numel()):
-        raise ValueError("out: expected [n, d] with unit channel stride")
+    if out.get_device() != dev or out.dim() != 2 or out.shape[0] != n or out.shape[1] != d or (out.stride(1) != 1 and n):
+        raise ValueError("out: expected [n, d] with unit channel stride on the cache's device")
     if n:
-        _call(lib().fp4kv_kv_dequant_fp4, dev, packed.data_ptr(), scales.data_ptr(), cap, d, _addr(src_row), n,
-              out.data_ptr(), 1 if out.dtype == torch.float32 else 0, _stride(out, 0, d))
+        _call((_lib or lib()).fp4kv_kv_dequant_fp4, dev, packed_at, scales_at, cap, d, src_at, n, out.data_ptr(),
+              1 if f32 else 0, _stride(out, 0, d))
     return out
 
 
@@ -474,47 +498,48 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
     n_draft (optional) int32 [B]; idx (optional) int32 [B, top_k]: the prefix positions to
     attend (every one without it). Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
     None); tokens behind n_draft keep what their outputs held."""
-    _need(q, torch.bfloat16, "q")
+    dev = q.get_device()
+    if dev < 0:
+        raise TypeError("q: expected a CUDA tensor")
     if q.dim() != 4:
         raise ValueError("q: expected [B, T, H, d]")
-    dev = q.device
+    q_at = _take(q, torch.bfloat16, "q", dev)
     B, T, H, d = q.shape
-    _need(packed, torch.uint8, "packed", dev)
-    _need(scales, torch.uint8, "scales", dev)
+    packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
     cap = packed.shape[1]
     if packed.shape != (B, cap, d // 2) or scales.shape != (B, cap, d // 16):
         raise ValueError("packed [B, cap, d/2] and scales [B, cap, d/16] expected")
-    _need(prefix_lens, torch.int32, "prefix_lens", dev)
-    _need(tree_mask, torch.int64, "tree_mask", dev)
+    lens_at, mask_at = _take(prefix_lens, torch.int32, "prefix_lens", dev), _take(tree_mask, torch.int64, "tree_mask", dev)
     if prefix_lens.numel() != B or tree_mask.shape != (B, T):
         raise ValueError("prefix_lens [B] and tree_mask [B, T] expected")
+    drafts_at = idx_at = lse_at = None
     if n_draft is not None:
-        _need(n_draft, torch.int32, "n_draft", dev)
+        drafts_at = _take(n_draft, torch.int32, "n_draft", dev)
         if n_draft.numel() != B:
             raise ValueError("n_draft: expected [B]")
     top_k = 0
     if idx is not None:
-        _need(idx, torch.int32, "idx", dev)
+        idx_at = _take(idx, torch.int32, "idx", dev)
         if idx.dim() != 2 or idx.shape[0] != B:
             raise ValueError("idx: expected [B, top_k]")
         top_k = idx.shape[1]
     if out is None:
-        out = torch.zeros((B, T, H, d), dtype=torch.bfloat16, device=dev)
+        out = torch.zeros((B, T, H, d), dtype=torch.bfloat16, device=q.device)
     if lse is None and want_lse:
-        lse = torch.full((B, T, H), float("-inf"), dtype=torch.float32, device=dev)
-    _need(out, torch.bfloat16, "out", dev)
+        lse = torch.full((B, T, H), float("-inf"), dtype=torch.float32, device=q.device)
+    out_at = _take(out, torch.bfloat16, "out", dev)
     if out.shape != q.shape:
         raise ValueError("out: expected q's shape")
     if lse is not None:
-        _need(lse, torch.float32, "lse", dev)
+        lse_at = _take(lse, torch.float32, "lse", dev)
         if lse.shape != (B, T, H):
             raise ValueError("lse: expected [B, T, H]")
     if ws is None:
-        ws = alloc_workspace(workspace_bytes(OP_TREE_ATTN, B, cap, T * H, top_k), dev)
-    _need(ws, torch.uint8, "ws", dev)
-    _call(lib().fp4kv_tree_attn_decode, dev, q.data_ptr(), B, T, H, d, packed.data_ptr(), scales.data_ptr(), cap,
-          prefix_lens.data_ptr(), _addr(n_draft), tree_mask.data_ptr(), _addr(idx), top_k, sm_scale, out.data_ptr(),
-          _addr(lse), ws.data_ptr(), ws.numel())
+        with torch.cuda.device(dev):
+            ws = alloc_workspace(workspace_bytes(OP_TREE_ATTN, B, cap, T * H, top_k), q.device)
+    ws_at = _take(ws, torch.uint8, "ws", dev)
+    _call((_lib or lib()).fp4kv_tree_attn_decode, dev, q_at, B, T, H, d, packed_at, scales_at, cap, lens_at, drafts_at, mask_at,
+          idx_at, top_k, sm_scale, out_at, lse_at, ws_at, ws.numel())
     return out, lse
 
 

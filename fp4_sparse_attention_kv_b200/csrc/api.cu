@@ -2,6 +2,7 @@
 // The declarations, argument meaning, layouts and error behaviour are documented in
 // include/fp4kv.h. Nothing here allocates device memory or synchronises (except
 // fp4kv_workspace_status, a diagnostic call documented as synchronising).
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -38,11 +39,14 @@ fp4kv_status cuda_fail(cudaError_t e, const char* where) {
 }
 
 int num_sms() {
+  static std::atomic<int> known[64];  // per device, asked once
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  int n = 0;
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
     return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -661,7 +665,7 @@ fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, in
   cudaError_t e;
   {
     prof::Scope ps(0, static_cast<cudaStream_t>(stream));
-    e = fp4kv::launch_qkv_norm_rope(p, static_cast<cudaStream_t>(stream));
+    e = fp4kv::launch_qkv_norm_rope(p, num_sms(), static_cast<cudaStream_t>(stream));
   }
   if (e != cudaSuccess) return cuda_fail(e, "qkv_norm_rope_fp4");
   return ok();

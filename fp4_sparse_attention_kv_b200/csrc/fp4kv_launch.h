@@ -40,7 +40,7 @@ struct NormRopeParams {
   int64_t max_pos;
   double eps;
 };
-cudaError_t launch_qkv_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_qkv_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------------------
 // Indexer scoring (Full scan or pool gather), fused with the first-level histogram of the

@@ -26,7 +26,6 @@ __global__ void __launch_bounds__(kThreads) k_kv_dequant_fp4(const uint8_t* __re
                                                              int64_t n_rows, uint8_t* __restrict__ out,
                                                              int64_t out_row_bytes, int rows_per_block, int upr,
                                                              uint32_t magic) {
-  griddep_wait();  // the rows may come from the kernel before this one on the stream
   constexpr int kCh = kF32 ? 4 : 8;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int n_units = static_cast<int>(min(static_cast<int64_t>(rows_per_block), n_rows - row0)) * upr;
@@ -85,9 +84,10 @@ cudaError_t launch(const uint8_t* packed, const uint8_t* scales, int64_t cap_row
   const uint32_t magic = static_cast<uint32_t>((uint64_t(1) << 32) / upr + 1);
   const int64_t blocks = (n_rows + rows - 1) / rows;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(k_kv_dequant_fp4<kF32, kIter>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), stream, packed,
-                    scales, cap_rows, d, src_row, n_rows, static_cast<uint8_t*>(out), out_row_stride * (kF32 ? 4 : 2),
-                    rows, upr, magic);
+  k_kv_dequant_fp4<kF32, kIter><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+      packed, scales, cap_rows, d, src_row, n_rows, static_cast<uint8_t*>(out), out_row_stride * (kF32 ? 4 : 2), rows, upr,
+      magic);
+  return cudaGetLastError();
 }
 
 }  // namespace

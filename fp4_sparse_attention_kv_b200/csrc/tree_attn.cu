@@ -29,6 +29,8 @@
 // to 2^3 above the maximum; p is stored as p * 2^6 in fp16, so the row's largest is at least 2^3 and at
 // most 2^15: 11 bits each, and below 2^-14 a step of 2^-24, 2^-27 of the largest. The sums are fp32.
 // Every wait is bounded; on timeout a status bit is set and the kernel winds down.
+#include <atomic>
+
 #include "fp4kv_common.cuh"
 #include "fp4kv_launch.h"
 #include "fp4kv_quant.cuh"
@@ -983,8 +985,16 @@ int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_s
 }
 
 cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(k_tree_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  static std::atomic<uint64_t> set[4];  // devices whose kernel has its shared-memory limit (calls of any thread)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev >= 256 || !(set[dev >> 6].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_tree_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    if (dev < 256) set[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
