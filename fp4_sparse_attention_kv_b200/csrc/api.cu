@@ -617,8 +617,8 @@ fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, in
     return fail(FP4KV_ERR_INVALID_ARG, "negative n_tokens, cap_rows or max_pos");
   if (n_tokens > (int64_t(1) << 31)) return fail(FP4KV_ERR_UNSUPPORTED, "n_tokens=%lld above 2^31", (long long)n_tokens);
   if (d % 32 != 0 || d < 32 || d > 1024) return fail(FP4KV_ERR_UNSUPPORTED, "d=%d must be a multiple of 32 in [32, 1024]", d);
-  if (rope_dim % 16 != 0 || rope_dim < 0 || rope_dim > d)
-    return fail(FP4KV_ERR_UNSUPPORTED, "rope_dim=%d must be a multiple of 16 in [0, d]", rope_dim);
+  if (rope_dim % 16 != 0 || rope_dim < 0 || rope_dim > d || rope_dim > 512)
+    return fail(FP4KV_ERR_UNSUPPORTED, "rope_dim=%d must be a multiple of 16 in [0, min(d, 512)]", rope_dim);
   if (!(eps >= 1e-30 && eps < 1e30)) return fail(FP4KV_ERR_INVALID_ARG, "eps=%g outside [1e-30, 1e30)", eps);
   if (!q && !kv) return fail(FP4KV_ERR_INVALID_ARG, "null q and kv");
   if (q && (H < 1 || H > 128)) return fail(FP4KV_ERR_UNSUPPORTED, "H=%d outside [1, 128]", H);

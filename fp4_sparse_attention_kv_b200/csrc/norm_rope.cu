@@ -11,8 +11,9 @@
 //
 // Queries: a warp takes several heads of one token. With P = w c and Q = -+ w_partner s, formed once per
 // token, every channel is y = (x P + x_partner Q) r, two at a time in packed fp32 (outside the rotated
-// channels P = w, Q = 0), so no lane waits for the rotated ones. fp32, rounded once to bf16. The next
-// head's row is on its way while one is computed.
+// channels P = w, Q = 0), so no lane waits for the rotated ones. fp32, rounded once to bf16. Rows come
+// through a ring in shared memory, four passes ahead (in registers one ahead fitted: 241 us for 8,192
+// tokens of 64 heads).
 //
 // The KV row: y's nearest fp32 value is rounded to bf16 and that is quantised, so the cache holds
 // exactly what kv_quant_fp4 makes of kv_out. A code is decided by which side of a border a value
@@ -20,7 +21,8 @@
 // v of y is off by at most 4 x 2^-24 of mag, the sum of the magnitudes of its two terms (the product and
 // the sum rounded, r rounded, one product; one term and 2 x 2^-24 outside the rotated channels). Where v
 // lies nearer than that (6, or 3 units) to a bf16 rounding border, y is formed in fp64: one value in
-// thousands. (All rotated channels in fp64: 145 us instead of the figure below for 131,072 rows.)
+// thousands. The rotated groups of a warp's rows are done together, one to a lane, after the others
+// (beside the others four lanes in 32 worked on them: 1,150 instructions a row, 172 us for 131,072 rows).
 #include "fp4kv_common.cuh"
 #include "fp4kv_launch.h"
 #include "fp4kv_quant.cuh"
@@ -80,26 +82,22 @@ FP4KV_DEV int partner_unit(const NormRopeParams& p, int c0, bool& second) {
 // ---------------------------------------------------------------------------------------
 // queries
 // ---------------------------------------------------------------------------------------
-// One group's x (words 0-7) and, for pairs of halves, its partners (8-15).
-template <int kPairs>
-FP4KV_DEV void load_group(const NormRopeParams& p, const uint16_t* xr, int c0, bool rot, uint32_t (&x)[8], uint32_t (&xp)[8]) {
-  const uint4 a = ld_v4(xr + c0), b = ld_v4(xr + c0 + 8);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  if (kPairs == kHalves) {
-    uint4 e = make_uint4(0, 0, 0, 0), f = e;
-    if (rot) {
-      bool second;
-      e = ld_v4(xr + partner_unit(p, c0, second));
-      f = ld_v4(xr + partner_unit(p, c0 + 8, second));
-    }
-    xp[0] = e.x; xp[1] = e.y; xp[2] = e.z; xp[3] = e.w;
-    xp[4] = f.x; xp[5] = f.y; xp[6] = f.z; xp[7] = f.w;
-  }
+FP4KV_DEV void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+FP4KV_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+FP4KV_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+FP4KV_DEV uint4 lds_v4(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
 }
 
 template <int LPR, int GPL, int kPairs>
-FP4KV_DEV void query_heads(const NormRopeParams& p, int64_t tok, int h0, int h1) {
+FP4KV_DEV void query_heads(const NormRopeParams& p, uint32_t ring, int64_t tok, int h0, int h1) {
+  constexpr int kDepth = 4 / GPL;             // passes in flight
+  constexpr uint32_t kSlot = 1024 * GPL;       // bytes of one: the rows at once, LPR * GPL groups of 32 each
   constexpr int kRows = 32 / LPR;  // heads at once
   const int l = threadIdx.x & (LPR - 1), sub = (threadIdx.x & 31) / LPR;
   if (kPairs != kNone && (p.positions[tok] < 0 || p.positions[tok] >= p.max_pos)) return;
@@ -157,18 +155,43 @@ FP4KV_DEV void query_heads(const NormRopeParams& p, int64_t tok, int h0, int h1)
   const uint16_t* xt = p.q + tok * p.q_tok_stride;
   uint16_t* yt = p.q_out + tok * p.H * p.d;
   const float eps = static_cast<float>(p.eps), inv_d = 1.0f / static_cast<float>(p.d);
-  uint32_t x[GPL][8] = {}, xp[GPL][8] = {};
-  if (h0 + sub < h1)
+  const int lane = threadIdx.x & 31;
+  // A pass's rows into a slot: each lane a unit of 16 bytes of each 512, wherever its row is.
+  auto fetch = [&](int h, uint32_t slot) {
 #pragma unroll
-    for (int g = 0; g < GPL; ++g)
-      if (there[g]) load_group<kPairs>(p, xt + (h0 + sub) * p.q_head_stride, (l + LPR * g) * kGroup, rot[g], x[g], xp[g]);
+    for (int i = 0; i < 2 * GPL; ++i) {
+      const int u = lane + 32 * i, row = u / (2 * LPR * GPL), at = u - row * (2 * LPR * GPL);
+      if (h + row < h1 && 8 * at < p.d) cp_async_16(slot + 16 * u, xt + (h + row) * p.q_head_stride + 8 * at);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch(h0 + i * kRows, ring + i * kSlot);  // (none behind h1)
+  uint32_t slot = ring;
 #pragma unroll 1
-  for (int h = h0 + sub; h - sub < h1; h += kRows) {
-    uint32_t nx[GPL][8] = {}, np[GPL][8] = {};  // the next head's
-    if (h + kRows < h1)
+  for (int hb = h0; hb < h1; hb += kRows) {
+    cp_async_wait<kDepth - 1>();
+    __syncwarp();
+    const uint32_t row = slot + sub * (32 * LPR * GPL);
+    uint32_t x[GPL][8], xp[GPL][8];
 #pragma unroll
-      for (int g = 0; g < GPL; ++g)
-        if (there[g]) load_group<kPairs>(p, xt + (h + kRows) * p.q_head_stride, (l + LPR * g) * kGroup, rot[g], nx[g], np[g]);
+    for (int g = 0; g < GPL; ++g) {
+      const int c0 = (l + LPR * g) * kGroup;
+      uint4 a = make_uint4(0, 0, 0, 0), b = a, e = a, f = a;
+      if (there[g]) {
+        a = lds_v4(row + 2 * c0);
+        b = lds_v4(row + 2 * c0 + 16);
+      }
+      if (kPairs == kHalves && rot[g]) {
+        bool second;
+        e = lds_v4(row + 2 * partner_unit(p, c0, second));
+        f = lds_v4(row + 2 * partner_unit(p, c0 + 8, second));
+      }
+      x[g][0] = a.x; x[g][1] = a.y; x[g][2] = a.z; x[g][3] = a.w;
+      x[g][4] = b.x; x[g][5] = b.y; x[g][6] = b.z; x[g][7] = b.w;
+      xp[g][0] = e.x; xp[g][1] = e.y; xp[g][2] = e.z; xp[g][3] = e.w;
+      xp[g][4] = f.x; xp[g][5] = f.y; xp[g][6] = f.z; xp[g][7] = f.w;
+    }
     uint64_t s2 = 0;
 #pragma unroll
     for (int g = 0; g < GPL; ++g)
@@ -181,7 +204,10 @@ FP4KV_DEV void query_heads(const NormRopeParams& p, int64_t tok, int h0, int h1)
     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(fmaf(ss, inv_d, eps));
     const uint64_t r2 = pack2(r, r);
-    __syncwarp();  // every lane has its row's partners: a row may be written over itself
+    __syncwarp();  // (every lane has read the slot; a row may be written over itself: it is here already)
+    fetch(hb + kDepth * kRows, slot);
+    slot = slot + kSlot == ring + kDepth * kSlot ? ring : slot + kSlot;
+    const int h = hb + sub;
 #pragma unroll
     for (int g = 0; g < GPL; ++g) {
       if (!there[g] || h >= h1) continue;
@@ -199,159 +225,239 @@ FP4KV_DEV void query_heads(const NormRopeParams& p, int64_t tok, int h0, int h1)
       *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(out + 8) = make_uint4(y[4], y[5], y[6], y[7]);
     }
-#pragma unroll
-    for (int g = 0; g < GPL; ++g)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[g][k] = nx[g][k];
-        xp[g][k] = np[g][k];
-      }
   }
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------------------
 // KV rows
 // ---------------------------------------------------------------------------------------
-// u: the channel's value over r, mag: the sum of its terms' magnitudes (at least |u|)
+// v: the quick form of a rotated channel; mag_r: the magnitudes of its two terms
 FP4KV_DEV bool near_border(float v, float mag_r) {
   const int off = static_cast<int>(__float_as_uint(v) & 0xffffu) - 0x8000;
   return static_cast<float>(abs(off)) * fabsf(v) <= 6.0f * mag_r;
 }
-
-template <int LPR, int GPL, int kPairs>
-FP4KV_DEV void kv_row(const NormRopeParams& p, int64_t tok) {
-  const int l = threadIdx.x & (LPR - 1);
-  const int groups = p.d / kGroup;
-  bool live = tok < p.n_tokens;
-  int64_t pos = 0;
-  if (kPairs != kNone && live) {
-    pos = p.positions[tok];
-    live = pos >= 0 && pos < p.max_pos;
+FP4KV_DEV uint32_t add_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A finished group to where it goes.
+FP4KV_DEV void store_group(const NormRopeParams& p, int64_t tok, int64_t dst, int gi, const uint32_t (&y)[8]) {
+  if (p.kv_out) {
+    uint16_t* out = p.kv_out + tok * p.d + gi * kGroup;
+    *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(out + 8) = make_uint4(y[4], y[5], y[6], y[7]);
   }
-  int64_t dst = -1;
-  if (live && p.packed) {
-    dst = p.dst_row ? p.dst_row[tok] : tok;
-    if (dst >= p.cap_rows) dst = -1;
+  if (dst >= 0) {
+    uint2 pk;
+    uint32_t sc;
+    quant_group(y, pk, sc);
+    *reinterpret_cast<uint2*>(p.packed + dst * (p.d / 2) + gi * 8) = pk;
+    p.scales[dst * (p.d / kGroup) + gi] = static_cast<uint8_t>(sc);
   }
+}
+// A rotated group of channels [c0, +16) of a row; the whole warp calls it (lanes with nothing to do: !on).
+template <int kPairs>
+FP4KV_DEV void rotated_group(const NormRopeParams& p, bool on, int64_t tok, int64_t dst, int64_t pos, int c0, double rd) {
   const uint16_t* xr = p.kv + tok * p.kv_stride;
-  uint32_t x[GPL][8], xp[GPL][8];
-  double s0 = 0.0, s1 = 0.0;
+  const int hr = p.rope_dim / 2, j0 = c0 - (p.d - p.rope_dim);
+  uint32_t x[8], w[8], xp[8], wp[8];
+  float co[16], si[16];  // kNeighbours: of pair k; kHalves: of channel k
+  bool second[2] = {false, false};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(kOnes, kOnes, kOnes, kOnes), e = a, f = b;
+    float4 c[2] = {}, s[2] = {};
+    if (on) {
+      a = ld_v4(xr + c0 + 8 * u);
+      if (p.kv_weight) b = ld_v4(p.kv_weight + c0 + 8 * u);
+      int jj = j0 / 2 + 4 * u;
+      if (kPairs == kHalves) {
+        const int cp = partner_unit(p, c0 + 8 * u, second[u]);
+        e = ld_v4(xr + cp);
+        if (p.kv_weight) f = ld_v4(p.kv_weight + cp);
+        jj = j0 + 8 * u - (second[u] ? hr : 0);
+      }
+      const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + pos * p.rope_dim + jj);
+      const float4* sn = reinterpret_cast<const float4*>(p.cos_sin + pos * p.rope_dim + hr + jj);
+      c[0] = cs[0];
+      s[0] = sn[0];
+      if (kPairs == kHalves) {
+        c[1] = cs[1];
+        s[1] = sn[1];
+      }
+    }
+    x[4 * u] = a.x; x[4 * u + 1] = a.y; x[4 * u + 2] = a.z; x[4 * u + 3] = a.w;
+    w[4 * u] = b.x; w[4 * u + 1] = b.y; w[4 * u + 2] = b.z; w[4 * u + 3] = b.w;
+    xp[4 * u] = e.x; xp[4 * u + 1] = e.y; xp[4 * u + 2] = e.z; xp[4 * u + 3] = e.w;
+    wp[4 * u] = f.x; wp[4 * u + 1] = f.y; wp[4 * u + 2] = f.z; wp[4 * u + 3] = f.w;
+    constexpr int n = kPairs == kHalves ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < n / 4; ++i) {
+      co[n * u + 4 * i] = c[i].x; co[n * u + 4 * i + 1] = c[i].y; co[n * u + 4 * i + 2] = c[i].z; co[n * u + 4 * i + 3] = c[i].w;
+      si[n * u + 4 * i] = s[i].x; si[n * u + 4 * i + 1] = s[i].y; si[n * u + 4 * i + 2] = s[i].z; si[n * u + 4 * i + 3] = s[i].w;
+    }
+  }
+  __syncwarp();  // every lane has its partners: a row may be written over itself
+  if (!on) return;
+  const float rf = static_cast<float>(rd);
+  // me c + other s (s with its sign)
+  auto turn = [&](float me, float other, float c, float s) -> uint32_t {
+    const float os = other * s;
+    const float v = fmaf(me, c, os) * rf;
+    if (near_border(v, (fabsf(me * c) + fabsf(os)) * rf))
+      return f64_to_bf16(fma(static_cast<double>(me), static_cast<double>(c), static_cast<double>(other) * s) * rd);
+    return f32_to_bf16(v);
+  };
+  uint32_t y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float a = half_of(x[k], 0) * half_of(w[k], 0), b = half_of(x[k], 1) * half_of(w[k], 1);
+    if (kPairs == kNeighbours) {
+      y[k] = turn(a, b, co[k], -si[k]) | (turn(b, a, co[k], si[k]) << 16);
+    } else {
+      const float ap = half_of(xp[k], 0) * half_of(wp[k], 0), bp = half_of(xp[k], 1) * half_of(wp[k], 1);
+      const bool sec = second[k >> 2];
+      y[k] = turn(a, ap, co[2 * k], sec ? si[2 * k] : -si[2 * k]) |
+             (turn(b, bp, co[2 * k + 1], sec ? si[2 * k + 1] : -si[2 * k + 1]) << 16);
+    }
+  }
+  store_group(p, tok, dst, c0 / kGroup, y);
+}
+
+// kPasses passes of 32 / LPR rows by one warp, from row row0 on.
+template <int LPR, int GPL, int kPairs, int kPasses>
+FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
+  constexpr int kRows = 32 / LPR, kBatch = kRows * kPasses;
+  static_assert(kBatch <= 32, "a lane per row");
+  const int lane = threadIdx.x & 31, l = lane & (LPR - 1), sub = lane / LPR;
+  const int groups = p.d / kGroup, plain = (p.d - p.rope_dim) / kGroup;
+  // lane i: row i's place, position and r
+  int64_t my_dst = -1, my_pos = 0;
+  bool my_live = false;
+  if (lane < kBatch && row0 + lane < p.n_tokens) {
+    my_live = true;
+    if (kPairs != kNone) {
+      my_pos = p.positions[row0 + lane];
+      my_live = my_pos >= 0 && my_pos < p.max_pos;
+    }
+    if (my_live && p.packed) {
+      my_dst = p.dst_row ? p.dst_row[row0 + lane] : row0 + lane;
+      if (my_dst >= p.cap_rows) my_dst = -1;
+    }
+  }
+  const uint32_t live_rows = __ballot_sync(0xffffffffu, my_live);
+  uint32_t x[kPasses][GPL][8];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+    for (int g = 0; g < GPL; ++g) {
+      const int r = i * kRows + sub, c0 = (l + LPR * g) * kGroup;
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (((live_rows >> r) & 1) && c0 < p.d) {
+        const uint16_t* xr = p.kv + (row0 + r) * p.kv_stride + c0;
+        a = ld_v4(xr);
+        b = ld_v4(xr + 8);
+      }
+      x[i][g][0] = a.x; x[i][g][1] = a.y; x[i][g][2] = a.z; x[i][g][3] = a.w;
+      x[i][g][4] = b.x; x[i][g][5] = b.y; x[i][g][6] = b.z; x[i][g][7] = b.w;
+    }
+  double my_r = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+    for (int g = 0; g < GPL; ++g)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // |x| as fp64 by its bits (a zero becomes 2^-127, whose square is nothing beside eps)
+        const double a = __hiloint2double(static_cast<int>(((x[i][g][k] & 0x7fffu) << 13) + (896u << 20)), 0);
+        const double b = __hiloint2double(static_cast<int>(((x[i][g][k] >> 3) & 0x0fffe000u) + (896u << 20)), 0);
+        s0 = fma(a, a, s0);
+        s1 = fma(b, b, s1);
+      }
+    double ss = s0 + s1;
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // (row i * kRows + k's sum lies in the lanes from k * LPR on)
+    ss = __shfl_sync(0xffffffffu, ss, (lane & (kRows - 1)) * LPR);
+    if (lane / kRows == i) my_r = ss;
+  }
+  my_r = rsqrt(my_r / p.d + p.eps);
+  uint32_t w[GPL][8];
 #pragma unroll
   for (int g = 0; g < GPL; ++g) {
     const int c0 = (l + LPR * g) * kGroup;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[g][k] = xp[g][k] = 0;
-    if (live && c0 < p.d) load_group<kPairs>(p, xr, c0, kPairs != kNone && c0 >= p.d - p.rope_dim, x[g], xp[g]);
+    uint4 a = make_uint4(kOnes, kOnes, kOnes, kOnes), b = a;
+    if (p.kv_weight && c0 < p.d) {
+      a = ld_v4(p.kv_weight + c0);
+      b = ld_v4(p.kv_weight + c0 + 8);
+    }
+    w[g][0] = a.x; w[g][1] = a.y; w[g][2] = a.z; w[g][3] = a.w;
+    w[g][4] = b.x; w[g][5] = b.y; w[g][6] = b.z; w[g][7] = b.w;
   }
 #pragma unroll
-  for (int g = 0; g < GPL; ++g)
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + sub;
+    const double rd = __shfl_sync(0xffffffffu, my_r, r);
+    const int64_t dst = __shfl_sync(0xffffffffu, my_dst, r);
+    const float rf = static_cast<float>(rd);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // |x| as fp64 by its bits (a zero becomes 2^-127, whose square is nothing beside eps)
-      const double a = __hiloint2double(static_cast<int>(((x[g][k] & 0x7fffu) << 13) + (896u << 20)), 0);
-      const double b = __hiloint2double(static_cast<int>(((x[g][k] >> 3) & 0x0fffe000u) + (896u << 20)), 0);
-      s0 = fma(a, a, s0);
-      s1 = fma(b, b, s1);
-    }
-  double ss = s0 + s1;
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double rd = rsqrt(ss / p.d + p.eps);
-  const float rf = static_cast<float>(rd);
-  __syncwarp();  // every lane has its row's partners: a row may be written over itself
-#pragma unroll
-  for (int g = 0; g < GPL; ++g) {
-    const int gi = l + LPR * g, c0 = gi * kGroup;
-    if (!live || gi >= groups) continue;
-    uint32_t y[8];
-    uint32_t w[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint4 wv = p.kv_weight ? ld_v4(p.kv_weight + c0 + 8 * u) : make_uint4(kOnes, kOnes, kOnes, kOnes);
-      w[4 * u] = wv.x; w[4 * u + 1] = wv.y; w[4 * u + 2] = wv.z; w[4 * u + 3] = wv.w;
-    }
-    if (kPairs != kNone && c0 >= p.d - p.rope_dim) {
-      const float* cs = p.cos_sin + pos * p.rope_dim;
-      const int hr = p.rope_dim / 2, j0 = c0 - (p.d - p.rope_dim);
-      // me c + other s (s with its sign)
-      auto turn = [&](float me, float other, float co, float si) -> uint32_t {
-        const float os = other * si;
-        const float v = fmaf(me, co, os) * rf;
-        if (near_border(v, (fabsf(me * co) + fabsf(os)) * rf))
-          return f64_to_bf16(fma(static_cast<double>(me), static_cast<double>(co), static_cast<double>(other) * si) * rd);
-        return f32_to_bf16(v);
-      };
-      if (kPairs == kNeighbours) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float co = cs[j0 / 2 + k], si = cs[hr + j0 / 2 + k];
-          const float a = half_of(x[g][k], 0) * half_of(w[k], 0), b = half_of(x[g][k], 1) * half_of(w[k], 1);
-          y[k] = turn(a, b, co, -si) | (turn(b, a, co, si) << 16);
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          bool second;
-          const int cp = partner_unit(p, c0 + 8 * u, second);
-          const int jj = j0 + 8 * u - (second ? hr : 0);
-          const uint4 pw = p.kv_weight ? ld_v4(p.kv_weight + cp) : make_uint4(kOnes, kOnes, kOnes, kOnes);
-          const uint32_t wp[4] = {pw.x, pw.y, pw.z, pw.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t e[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float si = cs[hr + jj + 2 * k + i];
-              e[i] = turn(half_of(x[g][4 * u + k], i) * half_of(w[4 * u + k], i), half_of(xp[g][4 * u + k], i) * half_of(wp[k], i),
-                          cs[jj + 2 * k + i], second ? si : -si);
-            }
-            y[4 * u + k] = e[0] | (e[1] << 16);
-          }
-        }
-      }
-    } else {
+    for (int g = 0; g < GPL; ++g) {
+      const int gi = l + LPR * g;
+      if (!((live_rows >> r) & 1) || gi >= plain) continue;
+      uint32_t y[8], near = 0xffffffffu;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float u0 = half_of(x[g][k], 0) * half_of(w[k], 0), u1 = half_of(x[g][k], 1) * half_of(w[k], 1);
-        const float v0 = u0 * rf, v1 = u1 * rf;
+        const float v0 = half_of(x[i][g][k], 0) * half_of(w[g][k], 0) * rf, v1 = half_of(x[i][g][k], 1) * half_of(w[g][k], 1) * rf;
         y[k] = f32x2_to_bf16x2(v0, v1);
-        // too near a rounding border for fp32 to tell
-        const bool n0 = (__float_as_uint(v0) & 0xffffu) - 0x7ffdu <= 6u, n1 = (__float_as_uint(v1) & 0xffffu) - 0x7ffdu <= 6u;
-        if (n0 || n1) {
-          if (n0) y[k] = (y[k] & 0xffff0000u) | f64_to_bf16(static_cast<double>(u0) * rd);
-          if (n1) y[k] = (y[k] & 0xffffu) | (f64_to_bf16(static_cast<double>(u1) * rd) << 16);
+        // the low halves, 0 .. 6 where within 3 units of a rounding border (0x8000)
+        near = __vminu2(near, add_u16x2(__byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x5410), 0x80038003u));
+      }
+      if (min(near & 0xffffu, near >> 16) <= 6u) {  // too near for fp32 to tell
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float u0 = half_of(x[i][g][k], 0) * half_of(w[g][k], 0), u1 = half_of(x[i][g][k], 1) * half_of(w[g][k], 1);
+          y[k] = f64_to_bf16(static_cast<double>(u0) * rd) | (f64_to_bf16(static_cast<double>(u1) * rd) << 16);
         }
       }
+      store_group(p, row0 + r, dst, gi, y);
     }
-    if (p.kv_out) {
-      uint16_t* out = p.kv_out + tok * p.d + c0;
-      *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(out + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-    }
-    if (dst >= 0) {
-      uint2 pk;
-      uint32_t sc;
-      quant_group(y, pk, sc);
-      *reinterpret_cast<uint2*>(p.packed + dst * (p.d / 2) + gi * 8) = pk;
-      p.scales[dst * groups + gi] = static_cast<uint8_t>(sc);
+  }
+  if (kPairs != kNone) {
+    // the rotated groups, one to a lane; a row's are all done in one step
+    const int rg = groups - plain, rows = 32 / rg;
+#pragma unroll 1
+    for (int first = 0; first < kBatch; first += rows) {
+      const int q = lane / rg, r = first + q;
+      const bool mine = q < rows && r < kBatch;
+      const int from = mine ? r : 0;
+      const double rd = __shfl_sync(0xffffffffu, my_r, from);
+      const int64_t dst = __shfl_sync(0xffffffffu, my_dst, from), pos = __shfl_sync(0xffffffffu, my_pos, from);
+      rotated_group<kPairs>(p, mine && ((live_rows >> from) & 1), row0 + from, dst, pos, (plain + lane - q * rg) * kGroup, rd);
     }
   }
 }
 
-template <int LPR, int GPL, int kPairs>
+// Rows of a KV warp: eight (four of more than 512 channels), whose rotated groups share the lanes; where
+// there are too few for every SM, as few as a pass has.
+template <int LPR, int GPL>
+constexpr int kKvPasses = (GPL == 1 ? 8 : 4) * LPR / 32;
+
+template <int LPR, int GPL, int kPairs, int kPasses>
 __global__ void __launch_bounds__(kThreads) k_kv_norm_rope(const NormRopeParams p) {
-  constexpr int kRows = 32 / LPR;  // rows of a warp
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  kv_row<LPR, GPL, kPairs>(p, warp * kRows + (threadIdx.x & 31) / LPR);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (kPasses * 32 / LPR);
+  if (row0 < p.n_tokens) kv_rows<LPR, GPL, kPairs, kPasses>(p, row0);
 }
 
 // The KV rows' blocks (more arithmetic each) come first, then the query heads', `heads` of a token per warp.
 template <int LPR, int GPL, int kPairs>
 __global__ void __launch_bounds__(kThreads, GPL == 1 ? 2 : 1) k_qkv_norm_rope(const NormRopeParams p, uint32_t kv_blocks, int heads) {
-  constexpr int kRows = 32 / LPR;
+  __shared__ __align__(128) uint8_t ring[kThreads / 32][4096];
   if (blockIdx.x < kv_blocks) {
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (warp * kRows < p.n_tokens) kv_row<LPR, GPL, kPairs>(p, warp * kRows + (threadIdx.x & 31) / LPR);
+    const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 / LPR);
+    if (row0 < p.n_tokens) kv_rows<LPR, GPL, kPairs, 1>(p, row0);
     return;
   }
   const int64_t unit = static_cast<int64_t>(blockIdx.x - kv_blocks) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -359,7 +465,16 @@ __global__ void __launch_bounds__(kThreads, GPL == 1 ? 2 : 1) k_qkv_norm_rope(co
   const int64_t tok = unit / parts;
   if (tok >= p.n_tokens) return;
   const int h0 = static_cast<int>(unit - tok * parts) * heads;
-  query_heads<LPR, GPL, kPairs>(p, tok, h0, min(h0 + heads, p.H));
+  query_heads<LPR, GPL, kPairs>(p, smem_u32(ring[threadIdx.x >> 5]), tok, h0, min(h0 + heads, p.H));
+}
+
+template <int LPR, int GPL, int kPairs, int kPasses>
+cudaError_t launch_kv(const NormRopeParams& p, cudaStream_t stream) {
+  const int64_t per_block = kPasses * (32 / LPR) * (kThreads / 32);
+  const int64_t blocks = (p.n_tokens + per_block - 1) / per_block;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  k_kv_norm_rope<LPR, GPL, kPairs, kPasses><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <int LPR, int GPL, int kPairs>
@@ -368,9 +483,9 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t per_block = kRows * (kThreads / 32);
   const int64_t kv_blocks = p.kv ? (p.n_tokens + per_block - 1) / per_block : 0;
   if (!p.q) {
-    if (kv_blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    k_kv_norm_rope<LPR, GPL, kPairs><<<static_cast<unsigned>(kv_blocks), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    constexpr int kMany = kKvPasses<LPR, GPL>;
+    return p.n_tokens >= int64_t(num_sms) * 16 * kMany * kRows ? launch_kv<LPR, GPL, kPairs, kMany>(p, stream)
+                                                               : launch_kv<LPR, GPL, kPairs, 1>(p, stream);
   }
   // heads per warp: one pass (kRows) where there are few rows, up to 16 passes where that leaves every SM
   // 32 warps to run

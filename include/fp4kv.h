@@ -274,7 +274,7 @@ fp4kv_status fp4kv_swa_quant_fp8(const uint16_t* x, int64_t n_rows, int32_t d, i
  * positions : int64 [n_tokens]; cos_sin: fp32 [max_pos][rope_dim], a position's cosines
  *             (rope_dim / 2), then its sines. Both unused with rope_dim == 0. A token whose
  *             position lies outside [0, max_pos) is skipped: all its outputs stay as they were.
- * d % 32 == 0, d <= 1024; rope_dim % 16 == 0, rope_dim <= d; 1 <= H <= 128; eps in
+ * d % 32 == 0, d <= 1024; rope_dim % 16 == 0, rope_dim <= min(d, 512); 1 <= H <= 128; eps in
  * [1e-30, 1e30). q, kv, the weights, the outputs and cos_sin are 16-byte aligned, strides
  * multiples of 8. */
 fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, int64_t q_head_stride, int32_t H,

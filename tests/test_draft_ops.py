@@ -156,7 +156,7 @@ def _norm_args(**k):
 
 @pytest.mark.parametrize("change, status, word", [
     (dict(d=48), 2, "d=48"), (dict(d=1056, kvs=1056), 2, "d=1056"), (dict(rope=24), 2, "rope_dim=24"),
-    (dict(rope=528), 2, "rope_dim=528"), (dict(rope=-16), 2, "rope_dim"), (dict(eps=0.0), 1, "eps"),
+    (dict(rope=528), 2, "rope_dim=528"), (dict(d=1024, kvs=1024, qhs=1024, rope=528), 2, "rope_dim=528"), (dict(rope=-16), 2, "rope_dim"), (dict(eps=0.0), 1, "eps"),
     (dict(eps=float("nan")), 1, "eps"), (dict(eps=float("inf")), 1, "eps"), (dict(q=None, kv=None), 1, "null q and kv"),
     (dict(H=0), 2, "H=0"), (dict(H=129), 2, "H=129"), (dict(qo=None), 1, "q_out"), (dict(packed=None), 1, "neither"),
     (dict(scales=None), 1, "scales"), (dict(pos=None), 1, "positions"), (dict(cs=None), 1, "cos_sin"),
@@ -304,7 +304,8 @@ def check_q(got, q, w, pos, table, rope, half, eps):
 @pytest.mark.parametrize("n, H, d, rope, half", [
     (1, 64, 512, 64, False), (1, 1, 32, 0, False), (3, 1, 32, 32, True), (130, 5, 64, 64, False), (777, 32, 128, 64, True),
     (33, 12, 96, 48, False), (33, 12, 96, 96, True), (50, 8, 192, 128, True), (64, 3, 256, 16, False),
-    (64, 128, 320, 0, False), (500, 2, 512, 512, True), (129, 16, 576, 64, False), (17, 7, 1024, 128, True),
+    (64, 128, 320, 0, False), (500, 2, 512, 512, True), (129, 16, 576, 64, False), (17, 7, 1024, 128, True), (40, 3, 1024, 512, True),
+    (20000, 0, 1024, 112, True), (40000, 0, 128, 48, True), (40000, 0, 192, 96, False), (30000, 0, 64, 0, False), (20000, 0, 512, 16, True),
     (5000, 0, 512, 64, True), (60000, 0, 512, 64, False)])
 def test_norm_rope(fk, n, H, d, rope, half, weight):
     q, kv, qw, kw = norm_inputs(n, H, d, n + d)
