@@ -447,6 +447,7 @@ constexpr int kKvPasses = (GPL == 1 ? 8 : 4) * LPR / 32;
 
 template <int LPR, int GPL, int kPairs, int kPasses>
 __global__ void __launch_bounds__(kThreads) k_kv_norm_rope(const NormRopeParams p) {
+  griddep_wait();
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (kPasses * 32 / LPR);
   if (row0 < p.n_tokens) kv_rows<LPR, GPL, kPairs, kPasses>(p, row0);
 }
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_norm_rope(const NormRopeParams 
 template <int LPR, int GPL, int kPairs>
 __global__ void __launch_bounds__(kThreads, GPL == 1 ? 2 : 1) k_qkv_norm_rope(const NormRopeParams p, uint32_t kv_blocks, int heads) {
   __shared__ __align__(128) uint8_t ring[kThreads / 32][4096];
+  griddep_wait();
   if (blockIdx.x < kv_blocks) {
     const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 / LPR);
     if (row0 < p.n_tokens) kv_rows<LPR, GPL, kPairs, 1>(p, row0);
@@ -473,8 +475,8 @@ cudaError_t launch_kv(const NormRopeParams& p, cudaStream_t stream) {
   const int64_t per_block = kPasses * (32 / LPR) * (kThreads / 32);
   const int64_t blocks = (p.n_tokens + per_block - 1) / per_block;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  k_kv_norm_rope<LPR, GPL, kPairs, kPasses><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_sized(kPasses == 1, k_kv_norm_rope<LPR, GPL, kPairs, kPasses>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                      stream, p);
 }
 
 template <int LPR, int GPL, int kPairs>
@@ -494,9 +496,8 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t units = p.n_tokens * ((p.H + heads - 1) / heads);
   const int64_t blocks = kv_blocks + (units + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  k_qkv_norm_rope<LPR, GPL, kPairs>
-      <<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p, static_cast<uint32_t>(kv_blocks), heads);
-  return cudaGetLastError();
+  return launch_sized(heads == kRows, k_qkv_norm_rope<LPR, GPL, kPairs>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), stream,
+                      p, static_cast<uint32_t>(kv_blocks), heads);
 }
 
 template <int kPairs>
