@@ -146,6 +146,7 @@ struct TreeAttnParams {
   uint16_t* out;              // [B][T][H][512] bf16
   float* lse;                 // nullable [B][T][H]
   int n_clusters, min_tiles;  // tree_clusters(), tree_min_tiles()
+  bool whole;                 // tree_whole_items(): items are not shared between clusters
   uint32_t* first_tile;       // workspace [B + 2]: each sequence's first tile, the number of tiles, the clusters in use
   float* part_ml;             // workspace [2 n_clusters][128][2]: reference and sum of unfinished items
   float* part_o;              // workspace [2 n_clusters][128][512]
@@ -156,6 +157,7 @@ struct TreeAttnParams {
 int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k);
 int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms);
 int tree_min_tiles();
+bool tree_whole_items(int64_t cap, int64_t top_k);
 cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------------------

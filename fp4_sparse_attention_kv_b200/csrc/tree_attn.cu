@@ -118,8 +118,13 @@ FP4KV_DEV void st_async_f32(uint32_t dst, float v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(dst), "f"(v), "r"(bar) : "memory");
 }
 
-FP4KV_DEV void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {  // 0 bytes: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+FP4KV_DEV void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+FP4KV_DEV uint4 lds_v4(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
 }
 FP4KV_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -214,7 +219,8 @@ struct Seq {
   uint32_t pre;    // rows of the prefix (cap < 2^31)
   uint32_t n_sel;  // entries before the drafts: the prefix, or the selection
   uint32_t tiles, groups;
-  FP4KV_DEV uint32_t work() const { return tiles * groups; }
+  // what the clusters share out: tiles, or whole items
+  FP4KV_DEV uint32_t work(bool whole) const { return whole ? (tiles ? groups : 0) : tiles * groups; }
 };
 FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
   Seq s;
@@ -256,7 +262,14 @@ struct alignas(16) SegIter {
   bool ready;         // the segment below is still to be done
   uint32_t g, tile0, nt;
   Seq s;
-  FP4KV_DEV void cut() {
+  FP4KV_DEV void cut(bool whole) {
+    if (whole) {
+      g = off++;
+      tile0 = 0;
+      nt = s.tiles;
+      --rem;
+      return;
+    }
     g = off / s.tiles;
     tile0 = off - g * s.tiles;
     nt = min(s.tiles - tile0, rem);
@@ -269,11 +282,11 @@ struct alignas(16) SegIter {
       return true;
     }
     if (rem == 0) return false;
-    while (off >= s.work()) {
-      off -= s.work();
+    while (off >= s.work(p.whole)) {
+      off -= s.work(p.whole);
       s = seq_of(p, ++b);
     }
-    cut();
+    cut(p.whole);
     return true;
   }
 };
@@ -362,14 +375,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   if (warp == 0) {
     Seq mine{};  // of sequence lane, then of the 32 at hand
     if (lane < p.B) mine = seq_of(p, lane);
-    uint32_t total = mine.work(), items = mine.groups;
-    uint32_t most = mine.work() ? mine.tiles : 0, least = mine.work() ? mine.tiles : 0xffffffffu;
+    uint32_t total = mine.work(p.whole), items = mine.groups;
+    uint32_t most = total ? mine.tiles : 0, least = total ? mine.tiles : 0xffffffffu;
 #pragma unroll 1
     for (int b = lane + 32; b < p.B; b += 32) {
       const Seq s = seq_of(p, b);
-      total += s.work();
+      total += s.work(p.whole);
       items += s.groups;
-      if (s.work()) {
+      if (s.work(p.whole)) {
         most = max(most, s.tiles);
         least = min(least, s.tiles);
       }
@@ -378,7 +391,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     items = __reduce_add_sync(0xffffffffu, items);
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
-    const uint32_t used = clusters_used(total, items, most == least ? most : 0, p.n_clusters, p.min_tiles);
+    const uint32_t used = p.whole ? max(1u, min(uint32_t(p.n_clusters), total))
+                                  : clusters_used(total, items, most == least ? most : 0, p.n_clusters, p.min_tiles);
     const uint32_t x0 = cl < used ? range_start(total, used, cl) : total;
     const uint32_t x1 = cl < used ? range_start(total, used, cl + 1) : total;
     // where x0 lies, and (cluster 0) each sequence's first tile for the merge
@@ -391,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         mine = Seq{};
         if (b < p.B) mine = seq_of(p, b);
       }
-      const uint32_t n = mine.work();
+      const uint32_t n = mine.work(p.whole);
       uint32_t incl = n;
 #pragma unroll 1
       for (int o = 1; o < 32 && o < p.B; o <<= 1) {
@@ -407,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           first.off = x0 - (at + incl - n);
           first.rem = x1 - x0;
           first.s = mine;
-          first.cut();
+          first.cut(p.whole);
           first.ready = true;
           *s_it = first;
         }
@@ -532,7 +546,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       load(ra, 0, e0);
       load(rb, 1, e1);
       if (seg == 0) join();
-      if (!values) ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);  // (Q came through the stages)
+      // (Q comes through the stages)
+      if (!values && !(seg == 0 && s.nd * p.H - static_cast<int>(it.g) * kRows <= 64))
+        ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);
       auto tile = [&](RawRow& r, uint32_t i) {
         if (!ok || i >= it.nt) return;
         // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
@@ -640,14 +656,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       bool ok = !aborted();
       if (!values) {
         // ------------------------------ scores and softmax ------------------------------
-        // ---- Q: bf16 -> fp16 times a power of two, in shared memory, then into TMEM ----
-        // (the last item's products are complete: its stages and Q's place are free)
+        // ---- Q: through shared memory into TMEM, bf16 -> fp16 times a power of two ----
+        // (The last item's products are complete: its stages and Q's place are free. Before the first item the
+        // slots of P are too, and hold 64 rows: then V need not wait.) Rows behind the last are not staged:
+        // what TMEM has in their place stays in their rows of S, which count as masked.
+        const uint32_t q_at = smem_u32(smem) + (seg == 0 && live_rows <= 64 ? kOffP : kOffV);
+        const int rows = min(live_rows, kRows);
 #pragma unroll 1
-        for (int r = warp; r < kRows; r += kSoftWarps) {
-          const uint16_t* src = p.q + (row0 + (r < live_rows ? r : 0)) * kD + 8 * lane;
-          const uint32_t dst = smem_u32(smem) + kOffV + r * 1024 + ((lane ^ (r & 7)) << 4);
-          cp_async_16(dst, src, r < live_rows ? 16 : 0);
-          cp_async_16(dst + 512, src + kD / 2, r < live_rows ? 16 : 0);
+        for (int r = warp; r < rows; r += kSoftWarps) {
+          const uint16_t* src = p.q + (row0 + r) * kD + 8 * lane;
+          const uint32_t dst = q_at + r * 1024 + ((lane ^ (r & 7)) << 4);
+          cp_async_16(dst, src);
+          cp_async_16(dst + 512, src + kD / 2);
         }
         uint64_t rmask = 0;  // the drafts that this row's token sees
         if (R < live_rows) {
@@ -660,44 +680,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           lane_addr = tmem + (uint32_t(32 * q) << 16);
         }
         cp_async_wait_all();
-        // (a negative scale goes into q's sign: the factor of the logits is positive)
-        const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll 1
-        for (int r = warp; r < kRows; r += kSoftWarps) {  // (each lane what it has copied itself)
-          uint8_t* at = smem + kOffV + r * 1024 + ((lane ^ (r & 7)) << 4);
-          const uint4 v0 = *reinterpret_cast<const uint4*>(at), v1 = *reinterpret_cast<const uint4*>(at + 512);
-          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-          uint32_t m2 = 0;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) m2 = __vmaxu2(m2, w[u] & 0x7fff7fffu);
+        for (int r = warp; r < rows; r += kSoftWarps) {  // a row's maximum (each lane of what it has copied itself)
+          const uint32_t at = q_at + r * 1024 + ((lane ^ (r & 7)) << 4);
+          const uint4 v0 = lds_v4(at), v1 = lds_v4(at + 512);
+          uint32_t m2 = __vmaxu2(__vmaxu2(v0.x & 0x7fff7fffu, v0.y & 0x7fff7fffu), __vmaxu2(v0.z & 0x7fff7fffu, v0.w & 0x7fff7fffu));
+          m2 = __vmaxu2(m2, __vmaxu2(v1.x & 0x7fff7fffu, v1.y & 0x7fff7fffu));
+          m2 = __vmaxu2(m2, __vmaxu2(v1.z & 0x7fff7fffu, v1.w & 0x7fff7fffu));
           const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
           // The power of two that brings the row's maximum into [2^14, 2^15), whose fp16 exponent is 29:
           // an exponent field x of bf16 becomes x - low (values of field low or less, below 2^-28 of the
           // maximum, come out wrong by up to 2^-29 of it).
-          const int low = max(int(m >> 7), 29) - 29;
-          const uint32_t low2 = static_cast<uint32_t>(low) * 0x00800080u;
-          uint32_t f[8];  // (field and mantissa three bits up, the sign beside them)
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            f[u] = ((__vmaxu2(w[u] & 0x7fff7fffu, low2) - low2) << 3) | ((w[u] ^ flip) & 0x80008000u);
-          *reinterpret_cast<uint4*>(at) = make_uint4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<uint4*>(at + 512) = make_uint4(f[4], f[5], f[6], f[7]);
-          if (lane == 0) sLow[r] = low;
+          if (lane == 0) sLow[r] = max(int(m >> 7), 29) - 29;
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
+        const int low = R < rows ? sLow[R] : 0;
+        {
+          const uint32_t low2 = static_cast<uint32_t>(low) * 0x00800080u;
+          // (a negative scale goes into q's sign: the factor of the logits is positive)
+          const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 f = *reinterpret_cast<const uint4*>(smem + kOffV + R * 1024 + (((16 * h4 + 4 * c + k) ^ (R & 7)) << 4));
-            w[4 * k] = f.x; w[4 * k + 1] = f.y; w[4 * k + 2] = f.z; w[4 * k + 3] = f.w;
+            for (int k = 0; k < 4; ++k) {
+              const uint4 f = lds_v4(q_at + R % (q_at == smem_u32(smem) + kOffP ? 64 : kRows) * 1024 + (((16 * h4 + 4 * c + k) ^ (R & 7)) << 4));
+              w[4 * k] = f.x; w[4 * k + 1] = f.y; w[4 * k + 2] = f.z; w[4 * k + 3] = f.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)  // (field and mantissa three bits up, the sign beside them)
+              w[k] = ((__vmaxu2(w[k] & 0x7fff7fffu, low2) - low2) << 3) | ((w[k] ^ flip) & 0x80008000u);
+            tmem_st16(lane_addr + 64 * h4 + 16 * c, w);
           }
-          tmem_st16(lane_addr + 64 * h4 + 16 * c, w);
         }
         tmem_st_wait();
         // q = fp16 * 2^(low - 112)
-        const int up = sLow[R] - 112;
+        const int up = low - 112;
         const float c = fmaxf(fabsf(p.sm_scale) * kLog2e * __uint_as_float(uint32_t(127 + up / 2) << 23) *
                                   __uint_as_float(uint32_t(127 + (up - up / 2)) << 23),
                               2e-38f);  // (above zero: a masked -inf stays -inf)
@@ -725,6 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           const uint32_t e0 = (it.tile0 + i) * kTile + kCols * h;
           if (e0 + kCols > s.n_sel)  // drafts among the columns
             vis |= e0 >= s.n_sel ? (e0 - s.n_sel < 64 ? uint32_t(rmask >> (e0 - s.n_sel)) : 0u) : uint32_t(rmask << (s.n_sel - e0));
+          if (R >= live_rows) vis = 0;
           dead = dead || !warp_wait(&bars[B_SFULL + sl], ph);
           tc_fence_after();
           uint32_t r[32];
@@ -974,13 +993,18 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
 
 int tree_min_tiles() { return 2; }
 
+// Items of few tiles are not shared between clusters: up to 10 tiles, the parts' way through the
+// workspace and the second launch cost as much as the tiles that are saved.
+bool tree_whole_items(int64_t cap, int64_t top_k) { return ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile <= 10; }
+
 int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k) {
   return B * ((rows + kRows - 1) / kRows) * (((top_k ? top_k : cap) + 64 + kTile - 1) / kTile);
 }
 
 int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms) {
-  const int64_t total = tree_tiles(B, rows, cap, top_k);
-  const int64_t most = (total + tree_min_tiles() - 1) / tree_min_tiles();
+  const int64_t most = tree_whole_items(cap, top_k)
+                           ? B * ((rows + kRows - 1) / kRows)
+                           : (tree_tiles(B, rows, cap, top_k) + tree_min_tiles() - 1) / tree_min_tiles();
   return static_cast<int>(most < num_sms / 2 ? most : num_sms / 2);
 }
 
@@ -1006,7 +1030,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_tree_attn, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   return launch_pdl(k_tree_merge, dim3(static_cast<unsigned>(p.B * ((p.T * p.H + 31) / 32)), kD / kMergeCh), dim3(256), stream, p);
 }
 
