@@ -546,9 +546,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       load(ra, 0, e0);
       load(rb, 1, e1);
       if (seg == 0) join();
-      // (Q comes through the stages)
-      if (!values && !(seg == 0 && s.nd * p.H - static_cast<int>(it.g) * kRows <= 64))
-        ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);
+      // (Q comes through the stages, but for a first item of up to 64 rows: then this wait comes at the end)
+      const bool q_apart = seg == 0 && s.nd * p.H - static_cast<int>(it.g) * kRows <= 64;
+      if (!values && !q_apart) ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);
       auto tile = [&](RawRow& r, uint32_t i) {
         if (!ok || i >= it.nt) return;
         // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
@@ -568,6 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         tile(ra, i);
         tile(rb, i + 1);
       }
+      if (!values && q_apart) ok = ok && warp_wait(&bars[B_QREADY], seg & 1);
       if (!ok) give_up();
       ++seg;
     }

@@ -409,6 +409,9 @@ def run_tree(fk, B, T, H, lens, drafts, cap, idx=None, seed=0, scale=512 ** -0.5
     (1, 16, 64, [4093], None, 4100),               # the cache ends inside the drafts
     (2, 4, 16, [50, 9999], None, 60),              # a length behind the cache's end
     (33, 2, 3, [(i * 37) % 200 for i in range(33)], None, 202),
+    (160, 1, 64, [(i * 29) % 150 for i in range(160)], None, 152),      # several short items to a cluster, 64 rows each
+    (90, 3, 64, [(i * 53) % 700 for i in range(90)], [1 + i % 3 for i in range(90)], 800),  # 64, 128 and 192 rows
+    (150, 2, 40, [(i * 61) % 900 for i in range(150)], None, 1000),     # parts of items, 80 rows each
 ])
 def test_tree_dense(fk, B, T, H, lens, drafts, cap):
     run_tree(fk, B, T, H, lens, drafts, cap, seed=B + T + H)
