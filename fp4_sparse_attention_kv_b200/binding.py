@@ -350,8 +350,9 @@ def swa_quant_fp8(x: torch.Tensor, out: torch.Tensor, dst_row: torch.Tensor | No
                                      _stream(x.device)))
 
 
-# The calls below check and marshal with as few Python operations as they can: for one token the
-# kernel takes less time than a careless check of ten tensors.
+# The calls below check and marshal with as few Python operations as they can (each costs 50 to 100 ns):
+# for one token the kernel takes less time than a careless check of ten tensors.
+_BF16, _FP32, _U8, _INT64, _INT32 = torch.bfloat16, torch.float32, torch.uint8, torch.int64, torch.int32
 _raw_stream, _raw_device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
 
 
@@ -366,12 +367,8 @@ def _call(fn, dev, *args):
         _check(st)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _take(t, dtype, name, dev):
-    """_need for a contiguous tensor on the device of index dev, its address."""
+    """_need for a contiguous tensor on the device of index dev; its address."""
     if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _need(t, dtype, name, torch.device("cuda", dev))
     return t.data_ptr()
@@ -379,9 +376,9 @@ def _take(t, dtype, name, dev):
 
 def _cache_rows(packed, scales, d):
     """Rows of a cache given as planes [..., d/2] and [..., d/16]."""
-    n, m = packed.numel(), scales.numel()
-    cap = 2 * n // d
-    if 2 * n != cap * d or 16 * m != cap * d:
+    n = 2 * packed.numel()
+    cap = n // d
+    if n != cap * d or 16 * scales.numel() != n:
         raise ValueError("packed / scales do not match d")
     return cap
 
@@ -398,70 +395,77 @@ def qkv_norm_rope_fp4(q, kv, *, positions=None, cos_sin=None, rope_dim=0, rope_h
     one = kv if q is None else q
     if one is None:
         raise ValueError("q or kv is required")
-    dev, n, d = one.get_device(), one.shape[0], one.shape[-1]
+    dev = one.get_device()
     if dev < 0:
         raise TypeError("q / kv: expected CUDA tensors")
-    bf16 = torch.bfloat16
-    H = qts = qhs = kvs = 0
-    q_at = kv_at = None
+    H = qts = qhs = kvs = max_pos = cap = 0
+    q_at = kv_at = qw_at = kw_at = pos_at = cs_at = qo_at = ko_at = dst_at = packed_at = scales_at = None
     if q is not None:
-        if q.dtype is not bf16 or q.dim() != 3 or (q.stride(2) != 1 and q.numel()):
-            raise TypeError("q: expected a bf16 [n, H, d] tensor with unit channel stride")
-        H = q.shape[1]
-        q_at, qts, qhs = q.data_ptr(), _stride(q, 0, H * d), _stride(q, 1, d)
-    if kv is not None:
-        if kv.dtype is not bf16 or kv.dim() != 2 or (kv.stride(1) != 1 and kv.numel()):
-            raise TypeError("kv: expected a bf16 [n, d] tensor with unit channel stride")
-        if kv.shape[0] != n or kv.shape[1] != d or kv.get_device() != dev:
-            raise ValueError("q [n, H, d] and kv [n, d] on one device expected")
-        kv_at, kvs = kv.data_ptr(), _stride(kv, 0, d)
-    qw_at = kw_at = pos_at = cs_at = qo_at = ko_at = dst_at = packed_at = scales_at = None
-    if q_weight is not None:
-        qw_at = _take(q_weight, bf16, "q_weight", dev)
-        if q_weight.numel() != d:
-            raise ValueError(f"q_weight: expected d = {d} values")
-    if kv_weight is not None:
-        kw_at = _take(kv_weight, bf16, "kv_weight", dev)
-        if kv_weight.numel() != d:
-            raise ValueError(f"kv_weight: expected d = {d} values")
-    max_pos = cap = 0
-    if rope_dim:
-        pos_at, cs_at = _take(positions, torch.int64, "positions", dev), _take(cos_sin, torch.float32, "cos_sin", dev)
-        if positions.numel() != n or cos_sin.dim() != 2 or cos_sin.shape[1] != rope_dim:
-            raise ValueError("positions [n] and cos_sin [max_pos, rope_dim] expected")
-        max_pos = cos_sin.shape[0]
-    if q is not None:
+        if q.dtype is not _BF16 or q.dim() != 3:
+            raise TypeError("q: expected a bf16 [n, H, d] tensor")
+        n, H, d = q.shape
+        qts, qhs, unit = q.stride()
+        if unit != 1 and q.numel():
+            raise ValueError("q: expected unit channel stride")
+        # (the stride of a dimension with one entry means nothing)
+        if n == 1:
+            qts = H * d
+        if H == 1:
+            qhs = d
+        q_at = q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((n, H, d), dtype=bf16, device=one.device)
-        qo_at = _take(q_out, bf16, "q_out", dev)
+            q_out = torch.empty((n, H, d), dtype=_BF16, device=q.device)
+        qo_at = _take(q_out, _BF16, "q_out", dev)
         if q_out.numel() != n * H * d:
             raise ValueError("q_out: expected [n, H, d]")
-    if kv is None:
-        if packed is not None or scales is not None or kv_out is not None:
-            raise ValueError("packed, scales and kv_out need kv")
-    else:
+        if q_weight is not None:
+            qw_at = _take(q_weight, _BF16, "q_weight", dev)
+            if q_weight.numel() != d:
+                raise ValueError(f"q_weight: expected d = {d} values")
+    if kv is not None:
+        if kv.dtype is not _BF16 or kv.dim() != 2:
+            raise TypeError("kv: expected a bf16 [n, d] tensor")
+        rows, width = kv.shape
+        kvs, unit = kv.stride()
+        if q is None:
+            n, d = rows, width
+        elif rows != n or width != d or kv.get_device() != dev:
+            raise ValueError("q [n, H, d] and kv [n, d] on one device expected")
+        if unit != 1 and kv.numel():
+            raise ValueError("kv: expected unit channel stride")
+        if n == 1:
+            kvs = d
+        kv_at = kv.data_ptr()
+        if kv_weight is not None:
+            kw_at = _take(kv_weight, _BF16, "kv_weight", dev)
+            if kv_weight.numel() != d:
+                raise ValueError(f"kv_weight: expected d = {d} values")
         if packed is not None or scales is not None:
-            packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
+            packed_at, scales_at = _take(packed, _U8, "packed", dev), _take(scales, _U8, "scales", dev)
             cap = _cache_rows(packed, scales, d)
             if dst_row is not None:
-                dst_at = _take(dst_row, torch.int64, "dst_row", dev)
+                dst_at = _take(dst_row, _INT64, "dst_row", dev)
                 if dst_row.numel() != n:
                     raise ValueError("dst_row: expected [n]")
         elif kv_out is None:
-            kv_out = torch.empty((n, d), dtype=bf16, device=one.device)
+            kv_out = torch.empty((n, d), dtype=_BF16, device=kv.device)
         if kv_out is not None:
-            ko_at = _take(kv_out, bf16, "kv_out", dev)
+            ko_at = _take(kv_out, _BF16, "kv_out", dev)
             if kv_out.numel() != n * d:
                 raise ValueError("kv_out: expected [n, d]")
+    elif packed is not None or scales is not None or kv_out is not None:
+        raise ValueError("packed, scales and kv_out need kv")
+    if rope_dim:
+        pos_at, cs_at = _take(positions, _INT64, "positions", dev), _take(cos_sin, _FP32, "cos_sin", dev)
+        if positions.numel() != n or cos_sin.dim() != 2:
+            raise ValueError("positions [n] and cos_sin [max_pos, rope_dim] expected")
+        max_pos, width = cos_sin.shape
+        if width != rope_dim:
+            raise ValueError("cos_sin: expected [max_pos, rope_dim]")
     if n:
         _call((_lib or lib()).fp4kv_qkv_norm_rope_fp4, dev, q_at, qts, qhs, H, qw_at, qo_at, kv_at, kvs, kw_at, ko_at, dst_at,
               packed_at, scales_at, cap, n, d, rope_dim, 1 if rope_half else 0, pos_at, cs_at, max_pos, eps)
     return q_out, kv_out
-
-
-def _stride(t, dim, alone):
-    """The stride of a dimension; one of a single entry, whose stride means nothing, counts as `alone`."""
-    return alone if t.shape[dim] == 1 else t.stride(dim)
 
 
 def kv_dequant_fp4(packed, scales, src_row=None, out=None, dtype=torch.bfloat16):
@@ -471,22 +475,25 @@ def kv_dequant_fp4(packed, scales, src_row=None, out=None, dtype=torch.bfloat16)
     dev, d = packed.get_device(), 2 * packed.shape[-1]
     if dev < 0:
         raise TypeError("packed: expected a CUDA tensor")
-    packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
+    packed_at, scales_at = _take(packed, _U8, "packed", dev), _take(scales, _U8, "scales", dev)
     n = cap = _cache_rows(packed, scales, d)
     src_at = None
     if src_row is not None:
-        src_at = _take(src_row, torch.int64, "src_row", dev)
+        src_at = _take(src_row, _INT64, "src_row", dev)
         n = src_row.numel()
     if out is None:
         out = torch.empty((n, d), dtype=dtype, device=packed.device)
-    f32 = out.dtype is torch.float32
-    if not f32 and out.dtype is not torch.bfloat16:
-        raise TypeError(f"out: expected bf16 or fp32, got {out.dtype}")
-    if out.get_device() != dev or out.dim() != 2 or out.shape[0] != n or out.shape[1] != d or (out.stride(1) != 1 and n):
-        raise ValueError("out: expected [n, d] with unit channel stride on the cache's device")
+    kind = out.dtype
+    if kind is not _BF16 and kind is not _FP32:
+        raise TypeError(f"out: expected bf16 or fp32, got {kind}")
+    if out.get_device() != dev or out.shape != (n, d):
+        raise ValueError("out: expected [n, d] on the cache's device")
     if n:
+        stride, unit = out.stride()
+        if unit != 1:
+            raise ValueError("out: expected unit channel stride")
         _call((_lib or lib()).fp4kv_kv_dequant_fp4, dev, packed_at, scales_at, cap, d, src_at, n, out.data_ptr(),
-              1 if f32 else 0, _stride(out, 0, d))
+              1 if kind is _FP32 else 0, d if n == 1 else stride)
     return out
 
 
@@ -503,23 +510,23 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
         raise TypeError("q: expected a CUDA tensor")
     if q.dim() != 4:
         raise ValueError("q: expected [B, T, H, d]")
-    q_at = _take(q, torch.bfloat16, "q", dev)
+    q_at = _take(q, _BF16, "q", dev)
     B, T, H, d = q.shape
-    packed_at, scales_at = _take(packed, torch.uint8, "packed", dev), _take(scales, torch.uint8, "scales", dev)
+    packed_at, scales_at = _take(packed, _U8, "packed", dev), _take(scales, _U8, "scales", dev)
     cap = packed.shape[1]
     if packed.shape != (B, cap, d // 2) or scales.shape != (B, cap, d // 16):
         raise ValueError("packed [B, cap, d/2] and scales [B, cap, d/16] expected")
-    lens_at, mask_at = _take(prefix_lens, torch.int32, "prefix_lens", dev), _take(tree_mask, torch.int64, "tree_mask", dev)
+    lens_at, mask_at = _take(prefix_lens, _INT32, "prefix_lens", dev), _take(tree_mask, _INT64, "tree_mask", dev)
     if prefix_lens.numel() != B or tree_mask.shape != (B, T):
         raise ValueError("prefix_lens [B] and tree_mask [B, T] expected")
     drafts_at = idx_at = lse_at = None
     if n_draft is not None:
-        drafts_at = _take(n_draft, torch.int32, "n_draft", dev)
+        drafts_at = _take(n_draft, _INT32, "n_draft", dev)
         if n_draft.numel() != B:
             raise ValueError("n_draft: expected [B]")
     top_k = 0
     if idx is not None:
-        idx_at = _take(idx, torch.int32, "idx", dev)
+        idx_at = _take(idx, _INT32, "idx", dev)
         if idx.dim() != 2 or idx.shape[0] != B:
             raise ValueError("idx: expected [B, top_k]")
         top_k = idx.shape[1]
@@ -527,17 +534,17 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
         out = torch.zeros((B, T, H, d), dtype=torch.bfloat16, device=q.device)
     if lse is None and want_lse:
         lse = torch.full((B, T, H), float("-inf"), dtype=torch.float32, device=q.device)
-    out_at = _take(out, torch.bfloat16, "out", dev)
+    out_at = _take(out, _BF16, "out", dev)
     if out.shape != q.shape:
         raise ValueError("out: expected q's shape")
     if lse is not None:
-        lse_at = _take(lse, torch.float32, "lse", dev)
+        lse_at = _take(lse, _FP32, "lse", dev)
         if lse.shape != (B, T, H):
             raise ValueError("lse: expected [B, T, H]")
     if ws is None:
         with torch.cuda.device(dev):
             ws = alloc_workspace(workspace_bytes(OP_TREE_ATTN, B, cap, T * H, top_k), q.device)
-    ws_at = _take(ws, torch.uint8, "ws", dev)
+    ws_at = _take(ws, _U8, "ws", dev)
     _call((_lib or lib()).fp4kv_tree_attn_decode, dev, q_at, B, T, H, d, packed_at, scales_at, cap, lens_at, drafts_at, mask_at,
           idx_at, top_k, sm_scale, out_at, lse_at, ws_at, ws.numel())
     return out, lse
