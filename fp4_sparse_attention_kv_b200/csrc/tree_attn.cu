@@ -312,9 +312,18 @@ FP4KV_DEV void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
       " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
-// dst: the chunk's row; x7: its number modulo 8 (the swizzle's phase).
-FP4KV_DEV void dequant_chunk(uint8_t* dst, int x7, const uint32_t (&c)[8], uint32_t s) {
-  uint32_t sc[4];
+// A chunk's row in shared memory, by lane j = 0 .. 3 of the four that share a row: unit k of 16 bytes goes to
+// position k ^ (row & 7) (the swizzle), and the lane writes its units in the order k ^ 2 j. That way a
+// row's 128 code bytes are read by neighbouring lanes (one line per eight lanes; eight rows to eight lanes
+// took four times the wavefronts), and eight lanes still write to distinct banks.
+// at: the row's address, with (row & 7) ^ 2 j in its unit bits.
+FP4KV_DEV void dequant_chunk(uint32_t at, uint32_t j, const uint32_t (&c)[8], uint32_t s) {
+  uint32_t v[8], w[8], sc[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = j & 1 ? c[k ^ 2] : c[k];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = j & 2 ? v[k ^ 4] : v[k];
+  s = __byte_perm(s, 0, 0x3210u ^ (0x1111u * j));
   const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(s & 0xffffu)), s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(s >> 16));
   sc[0] = __byte_perm(s01, 0, 0x1010);
   sc[1] = __byte_perm(s01, 0, 0x3232);
@@ -323,9 +332,10 @@ FP4KV_DEV void dequant_chunk(uint8_t* dst, int x7, const uint32_t (&c)[8], uint3
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     uint32_t h[4];
-    e2m1x8_to_f16(c[k], h);
-    *reinterpret_cast<uint4*>(dst + ((k ^ x7) << 4)) =
-        make_uint4(hmul2_f16(h[0], sc[k >> 1]), hmul2_f16(h[1], sc[k >> 1]), hmul2_f16(h[2], sc[k >> 1]), hmul2_f16(h[3], sc[k >> 1]));
+    e2m1x8_to_f16(w[k], h);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(at ^ (16u * k)), "r"(hmul2_f16(h[0], sc[k >> 1])), "r"(hmul2_f16(h[1], sc[k >> 1])),
+                   "r"(hmul2_f16(h[2], sc[k >> 1])), "r"(hmul2_f16(h[3], sc[k >> 1])) : "memory");
   }
 }
 
@@ -492,8 +502,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ------------------------------ load and dequantize ------------------------------
     more_registers<80>();
-    // Eight lanes take eight rows (distinct swizzle phases: no store conflicts), two chunks each.
-    const int row = 8 * (warp - kSoftWarps) + (lane & 7), j = lane >> 3, half = (warp - kSoftWarps) >> 2;
+    // Four lanes share a row, two chunks each.
+    const int row = 8 * (warp - kSoftWarps) + (lane >> 2), half = (warp - kSoftWarps) >> 2;
+    const uint32_t j = lane & 3;
+    const uint32_t unit0 = smem_u32(smem) + kOffV + j * kVChunk + row * 128 + (((row & 7) ^ (2 * j)) << 4);
     const bool al32 = (reinterpret_cast<uintptr_t>(p.packed) & 31) == 0;
     bool ok = true;
     while (it.next(p)) {
@@ -554,9 +566,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
         ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + 2 * st + half], sph ^ 1, 32));
         if (!ok) return;
-        uint8_t* dst = smem + kOffV + st * kVBytes + j * kVChunk + row * 128;
-        dequant_chunk(dst, row & 7, r.c[0], r.s[0]);
-        dequant_chunk(dst + 4 * kVChunk, row & 7, r.c[1], r.s[1]);
+        const uint32_t at = unit0 + st * kVBytes;
+        dequant_chunk(at, j, r.c[0], r.s[0]);
+        dequant_chunk(at + 4 * kVChunk, j, r.c[1], r.s[1]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_VFULL + 2 * st + half]);
