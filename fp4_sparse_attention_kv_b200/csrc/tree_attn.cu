@@ -368,7 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool values = cluster_ctarank() != 0;  // the CTA that makes O
   const uint32_t cl = blockIdx.x >> 1;
-  griddep_launch_dependents();  // (k_tree_merge, which waits for this grid before it reads anything)
+  // k_tree_merge waits for this grid before it reads anything; with whole items it isn't launched, and the kernel
+  // that then comes next may read what this one writes before its own wait (sparse_attn_decode its query)
+  if (!p.whole) griddep_launch_dependents();
   griddep_wait();
 
   // the smem alignment that the swizzled operands need (the same in both CTAs of a launch)

@@ -619,3 +619,37 @@ def test_norm_output_feeds_the_attention_at_once(fk):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
+
+
+@gpu
+@pytest.mark.parametrize("n", [200, 900])  # (items that stay whole, and items that are joined by a second launch)
+def test_tree_output_feeds_the_attention_at_once(fk, n):
+    """The tree's output as the query of sparse_attn_decode, with nothing between the two launches."""
+    H, d = 64, 512
+    packed, scales = make_cache(fk, 1, n, 33)
+    idx = torch.arange(128, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([n - 1], dtype=torch.int32, device=DEV)
+    mask = torch.ones(1, 1, dtype=torch.int64, device=DEV)
+    ws = fk.alloc_workspace(fk.workspace_bytes(fk.OP_SPARSE_ATTN, 1, n, H, 128), DEV)
+    tws = fk.alloc_workspace(fk.workspace_bytes(fk.OP_TREE_ATTN, 1, n, H, 0), DEV)
+    raw = [torch.randn(1, 1, H, d, generator=gen(60 + i), device=DEV).bfloat16() for i in range(8)]
+    mid = torch.empty(1, 1, H, d, dtype=torch.bfloat16, device=DEV)
+    outs = [torch.empty(1, H, d, device=DEV) for _ in raw]
+
+    def step(x, o, wait):
+        fk.tree_attn_decode(x, packed, scales, lens, mask, sm_scale=0.04, out=mid, ws=tws)
+        if wait:
+            torch.cuda.synchronize()
+        fk.sparse_attn_decode(mid.view(1, H, d), packed, scales, lens, idx, 0.04, ws=ws, out=o, want_lse=False)
+
+    want = []
+    for x, o in zip(raw, outs):
+        step(x, o, True)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+    for _ in range(5):
+        for x, o in zip(raw, outs):
+            step(x, o, False)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
