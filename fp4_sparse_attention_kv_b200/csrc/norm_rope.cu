@@ -232,10 +232,11 @@ FP4KV_DEV void query_heads(const NormRopeParams& p, uint32_t ring, int64_t tok, 
 // ---------------------------------------------------------------------------------------
 // KV rows
 // ---------------------------------------------------------------------------------------
+constexpr float kLeastR = 0x1p-120f;  // below it r as fp32 loses bits that the quick forms count on
 // v: the quick form of a rotated channel; mag_r: the magnitudes of its two terms
-FP4KV_DEV bool near_border(float v, float mag_r) {
+FP4KV_DEV bool near_border(float v, float mag_r, float units) {
   const int off = static_cast<int>(__float_as_uint(v) & 0xffffu) - 0x8000;
-  return static_cast<float>(abs(off)) * fabsf(v) <= 6.0f * mag_r;
+  return !(static_cast<float>(abs(off)) * fabsf(v) > units * mag_r);  // (also where v is NaN, as of two infinite terms)
 }
 FP4KV_DEV uint32_t add_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -301,12 +302,12 @@ FP4KV_DEV void rotated_group(const NormRopeParams& p, bool on, int64_t tok, int6
   }
   __syncwarp();  // every lane has its partners: a row may be written over itself
   if (!on) return;
-  const float rf = static_cast<float>(rd);
+  const float rf = static_cast<float>(rd), wide = rf < kLeastR ? INFINITY : 6.0f;
   // me c + other s (s with its sign)
   auto turn = [&](float me, float other, float c, float s) -> uint32_t {
     const float os = other * s;
     const float v = fmaf(me, c, os) * rf;
-    if (near_border(v, (fabsf(me * c) + fabsf(os)) * rf))
+    if (near_border(v, (fabsf(me * c) + fabsf(os)) * rf, wide))
       return f64_to_bf16(fma(static_cast<double>(me), static_cast<double>(c), static_cast<double>(other) * s) * rd);
     return f32_to_bf16(v);
   };
@@ -371,7 +372,8 @@ FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
     for (int g = 0; g < GPL; ++g)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        // |x| as fp64 by its bits (a zero becomes 2^-127, whose square is nothing beside eps)
+        // |x| as fp64 by its bits (a zero becomes 2^-127, whose square is nothing beside eps; an
+        // infinity or NaN at least 2^128: below)
         const double a = __hiloint2double(static_cast<int>(((x[i][g][k] & 0x7fffu) << 13) + (896u << 20)), 0);
         const double b = __hiloint2double(static_cast<int>(((x[i][g][k] >> 3) & 0x0fffe000u) + (896u << 20)), 0);
         s0 = fma(a, a, s0);
@@ -383,6 +385,21 @@ FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
     // (row i * kRows + k's sum lies in the lanes from k * LPR on)
     ss = __shfl_sync(0xffffffffu, ss, (lane & (kRows - 1)) * LPR);
     if (lane / kRows == i) my_r = ss;
+  }
+  if (__any_sync(0xffffffffu, my_r >= 0x1p255)) {  // a row that isn't finite, or one near the type's end
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int g = 0; g < GPL; ++g)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = __vmaxu2(m, x[i][g][k] & 0x7fff7fffu);
+      m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = __shfl_sync(0xffffffffu, m, (lane & (kRows - 1)) * LPR);
+      if (lane / kRows == i && m >= 0x7f80u) my_r = __hiloint2double(m == 0x7f80u ? 0x7ff00000 : 0x7ff80000, 0);
+    }
   }
   my_r = rsqrt(my_r / p.d + p.eps);
   uint32_t w[GPL][8];
@@ -407,7 +424,7 @@ FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
     for (int g = 0; g < GPL; ++g) {
       const int gi = l + LPR * g;
       if (!((live_rows >> r) & 1) || gi >= plain) continue;
-      uint32_t y[8], near = 0xffffffffu;
+      uint32_t y[8], near = rf < kLeastR ? 0 : 0xffffffffu;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float v0 = half_of(x[i][g][k], 0) * half_of(w[g][k], 0) * rf, v1 = half_of(x[i][g][k], 1) * half_of(w[g][k], 1) * rf;

@@ -256,7 +256,7 @@ fp4kv_status fp4kv_swa_quant_fp8(const uint16_t* x, int64_t n_rows, int32_t d, i
  * row in one launch; the KV row goes to the FP4 cache as it is made. (The pages do not say how
  * queries and rows are normed and rotated: this is the form that latent attention needs.) For
  * a row x of d channels with weight w (1 where NULL):
- *   r = 1 / sqrt(sum x^2 / d + eps),  u = x * w;
+ *   r = 1 / sqrt(sum x^2 / d + eps),  u = x * w (as fp32; exact within its range);
  *   the first d - rope_dim channels:  y_i = u_i * r;
  *   the last rope_dim in pairs (a, b) with the token's (c, s): y_a = (u_a c - u_b s) * r,
  *   y_b = (u_b c + u_a s) * r. The pairs are neighbours (2j, 2j + 1), or with rope_half != 0

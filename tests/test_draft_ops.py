@@ -337,6 +337,49 @@ def test_norm_rope(fk, n, H, d, rope, half, weight):
 
 
 @gpu
+@pytest.mark.parametrize("n, d", [(5, 128), (70000, 128), (9, 512), (20000, 512), (6, 1024)])
+def test_norm_rope_rows_that_are_not_finite(fk, n, d):
+    """By the formula a NaN channel makes its row NaN, and an infinite one (r = 0) zeros with NaN in its
+    own place (and, rotated, in its partner's). The cache holds what kv_quant_fp4 makes of that."""
+    rope = 32
+    x = torch.randn(n, d, generator=gen(71), device=DEV).bfloat16()
+    x[0, 3] = float("nan")
+    x[1, 0] = float("inf")
+    x[2, d - 1] = float("-inf")     # rotated with channel d - 2
+    x[n - 1, d - rope] = float("nan")
+    x[n - 2, d // 2] = 3.3e38       # finite
+    table = table_of(64, rope)
+    pos = torch.arange(n, device=DEV) % 64
+    packed, scales = (torch.zeros(n, d // k, dtype=torch.uint8, device=DEV) for k in (2, 16))
+    q, kv = fk.qkv_norm_rope_fp4(None, x, positions=pos, cos_sin=table, rope_dim=rope, packed=packed, scales=scales,
+                                 kv_out=torch.empty_like(x))
+    p2, s2 = torch.zeros_like(packed), torch.zeros_like(scales)
+    fk.kv_quant_fp4(kv, p2, s2)
+    assert torch.equal(packed, p2) and torch.equal(scales, s2)
+    want = bf16_of_f64(plain_norm_rope(x, None, pos, table, rope, False, 1e-6)[0])
+    assert torch.isnan(kv[0]).all() and torch.isnan(kv[n - 1]).all()
+    for r, places in ((1, [0]), (2, [d - 2, d - 1])):
+        nan = torch.zeros(d, dtype=torch.bool, device=DEV)
+        nan[places] = True
+        assert torch.isnan(kv[r][nan]).all() and (kv[r][~nan] == 0).all()
+    rest = torch.isfinite(x).all(1)
+    assert torch.equal(kv[rest].float(), want[rest].float())
+
+
+@gpu
+@pytest.mark.parametrize("half", [False, True])
+def test_norm_rope_rows_near_the_ends_of_the_type(fk, half):
+    """r below fp32's normal range (channels near 3e38), and rows of tiny channels: kv_out is exact."""
+    n, d, rope = 4096, 512, 64
+    x = torch.randn(n, d, generator=gen(72), device=DEV).clamp(-2, 2)
+    x = (x * torch.where(torch.arange(n, device=DEV) % 2 == 0, 1.6e38, 1e-33)[:, None]).bfloat16()
+    table, pos = table_of(64, rope), torch.arange(n, device=DEV) % 64
+    _, kv = fk.qkv_norm_rope_fp4(None, x, positions=pos, cos_sin=table, rope_dim=rope, rope_half=half)
+    want = bf16_of_f64(plain_norm_rope(x, None, pos, table, rope, half, 1e-6)[0])
+    assert torch.equal(kv.float(), want.float())
+
+
+@gpu
 def test_norm_rope_strides_in_place_and_tokens_left_alone(fk):
     n, H, d, rope = 40, 6, 128, 64
     g = gen(5)
