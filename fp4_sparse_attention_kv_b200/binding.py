@@ -531,9 +531,11 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
             raise ValueError("idx: expected [B, top_k]")
         top_k = idx.shape[1]
     if out is None:
-        out = torch.zeros((B, T, H, d), dtype=torch.bfloat16, device=q.device)
+        out = (torch.empty if n_draft is None else torch.zeros)((B, T, H, d), dtype=torch.bfloat16, device=q.device)
     if lse is None and want_lse:
-        lse = torch.full((B, T, H), float("-inf"), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+        if n_draft is not None:
+            lse.fill_(float("-inf"))
     out_at = _take(out, _BF16, "out", dev)
     if out.shape != q.shape:
         raise ValueError("out: expected q's shape")

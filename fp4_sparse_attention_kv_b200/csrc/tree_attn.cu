@@ -306,6 +306,10 @@ FP4KV_DEV void ld_nc_32b(uint32_t (&r)[8], const uint8_t* p, bool al32) {
     r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w; r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
   }
 }
+// Four E4M3 scales, a NaN (all bits but the sign) as 1.875.
+FP4KV_DEV uint32_t finite_scales(uint32_t s) {
+  return s & ~((((s & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 1);
+}
 // Eight codes -> four f16x2 (the byte registers spare the shifts).
 FP4KV_DEV void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
@@ -569,6 +573,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + 2 * st + half], sph ^ 1, 32));
         if (!ok) return;
         const uint32_t at = unit0 + st * kVBytes;
+        // A row with a NaN scale makes its logits NaN, so p is NaN for those who see it and 0 for the others; as a
+        // value it is read as finite, since 0 * NaN would reach the others too. (As the value CTA
+        // waits most of the time, this costs least here: 295 to 301 us for 4 x 1,024 query rows over 32,784.)
+        if (values) {
+          r.s[0] = finite_scales(r.s[0]);
+          r.s[1] = finite_scales(r.s[1]);
+        }
         dequant_chunk(at, j, r.c[0], r.s[0]);
         dequant_chunk(at + 4 * kVChunk, j, r.c[1], r.s[1]);
         fence_proxy_async_smem();
@@ -714,6 +725,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           const uint32_t low2 = static_cast<uint32_t>(low) * 0x00800080u;
           // (a negative scale goes into q's sign: the factor of the logits is positive)
           const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;
+          // (an infinity has no fp16 here, and no softmax: with it, or NaN, in the row all of q is NaN)
+          const uint32_t nan2 = low == 255 - 29 ? 0x7fff7fffu : 0u;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t w[16];
@@ -724,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k)  // (field and mantissa three bits up, the sign beside them)
-              w[k] = ((__vmaxu2(w[k] & 0x7fff7fffu, low2) - low2) << 3) | ((w[k] ^ flip) & 0x80008000u);
+              w[k] = ((__vmaxu2(w[k] & 0x7fff7fffu, low2) - low2) << 3) | ((w[k] ^ flip) & 0x80008000u) | nan2;
             tmem_st16(lane_addr + 64 * h4 + 16 * c, w);
           }
         }
@@ -879,7 +892,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         const bool whole = it.tile0 == 0 && it.nt == s.tiles;
         const bool live = R < live_rows;
         const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (NaN stays NaN)
         const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -918,7 +931,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           if (!whole)
             __stcg(reinterpret_cast<float2*>(p.part_ml) + slot * kRows + R, make_float2(ref, l));
           else if (p.lse)
-            p.lse[row0 + R] = l > 0.0f ? (ref - kPLog2) * kLn2 + logf(l) : -INFINITY;
+            p.lse[row0 + R] = l == 0.0f ? -INFINITY : (ref - kPLog2) * kLn2 + logf(l);
         }
         tc_fence_before();
         // every warp has read O, the reference and the sum: the next item may start, the slot is free
@@ -983,14 +996,14 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (NaN stays NaN)
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float* t = &tile[lane][4 * (warp + 8 * k)];
     t[0] = o[k].x * inv; t[1] = o[k].y * inv; t[2] = o[k].z * inv; t[3] = o[k].w * inv;
   }
   const int64_t row0 = int64_t(b) * p.T * p.H + r0;
-  if (p.lse && blockIdx.y == 0 && warp == 0 && live) p.lse[row0 + lane] = l > 0.0f ? (m - kPLog2) * kLn2 + logf(l) : -INFINITY;
+  if (p.lse && blockIdx.y == 0 && warp == 0 && live) p.lse[row0 + lane] = l == 0.0f ? -INFINITY : (m - kPLog2) * kLn2 + logf(l);
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

@@ -309,7 +309,9 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  * int32 [B]: sequence b drafts only its first n_draft[b] (clamped to [0, T]) tokens; q, mask
  * and outputs of the others are not touched, and mask bits at or above it are ignored. Prefix
  * lengths are clamped to [0, cap]; drafted rows at or behind cap are absent. A token that sees
- * nothing gets out = 0, lse = -inf. A row that no token sees is not read.
+ * nothing gets out = 0, lse = -inf. A row that no token sees is not read. A cache row with a NaN
+ * scale gives NaN to the tokens that see it and to no others; a query head with an infinity or
+ * NaN gives NaN (unless its token sees nothing).
  * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without;
  * B * ceil(T H / 128) * ceil((R + 64) / 64) < 2^32 with R = top_k or cap. ws: at least
  * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,

@@ -545,6 +545,48 @@ def test_tree_extreme_queries(fk):
 
 
 @gpu
+@pytest.mark.parametrize("n", [40, 900])  # (whole items, and items in parts)
+def test_tree_a_nan_row_reaches_only_those_who_see_it(fk, n):
+    """A drafted row whose scale is NaN, as the quantizer writes for a row with NaN: NaN for the tokens
+    that see it, nothing for the others."""
+    B, T, H = 1, 4, 40
+    packed, scales = make_cache(fk, B, n + T, 16)
+    mask = torch.tensor([[0b0001, 0b0011, 0b0101, 0b1101]], dtype=torch.int64, device=DEV)
+    q = torch.randn(B, T, H, 512, generator=gen(17), device=DEV).bfloat16()
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    want, wl = fk.tree_attn_decode(q, packed, scales, lens, mask, sm_scale=0.04)
+    bad = scales.clone()
+    bad[0, n + 2, 5] = 0x7F
+    bad[0, n + 2, 9] = 0xFF
+    out, lse = fk.tree_attn_decode(q, packed, bad, lens, mask, sm_scale=0.04)
+    assert torch.equal(out[:, :2], want[:, :2]) and torch.equal(lse[:, :2], wl[:, :2])
+    assert torch.isnan(out[:, 2:]).all() and torch.isnan(lse[:, 2:]).all()
+
+
+@gpu
+@pytest.mark.parametrize("n", [40, 900])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_tree_queries_that_are_not_finite(fk, n, value):
+    """NaN for their own head (softmax of infinite logits has no value), the others as they were; a token
+    that sees nothing gives 0 all the same."""
+    B, T, H = 2, 2, 70
+    packed, scales = make_cache(fk, B, n + T, 18)
+    mask = torch.tensor([[1, 2], [0, 3]], dtype=torch.int64, device=DEV)
+    q = torch.randn(B, T, H, 512, generator=gen(19), device=DEV).bfloat16()
+    lens = torch.tensor([n, 0], dtype=torch.int32, device=DEV)
+    want, wl = fk.tree_attn_decode(q, packed, scales, lens, mask, sm_scale=0.04)
+    x = q.clone()
+    hit = torch.zeros(B, T, H, dtype=torch.bool, device=DEV)
+    for b, t, h, c in [(0, 0, 0, 0), (0, 1, 69, 511), (0, 1, 3, 100), (1, 0, 5, 7), (1, 1, 64, 256)]:
+        x[b, t, h, c] = value
+        hit[b, t, h] = (b, t) != (1, 0)
+    out, lse = fk.tree_attn_decode(x, packed, scales, lens, mask, sm_scale=0.04)
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
+    assert (out[1, 0] == 0).all() and torch.isneginf(lse[1, 0]).all()
+
+
+@gpu
 def test_tree_binding_checks(fk):
     q, packed, scales, lt, mask, nd, out, lse = run_tree(fk, 1, 2, 4, [10], None, 12)
     o, l = fk.tree_attn_decode(q, packed, scales, lt, mask, sm_scale=512 ** -0.5)
