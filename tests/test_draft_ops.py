@@ -738,3 +738,87 @@ def test_tree_output_feeds_the_attention_at_once(fk, n):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
+
+
+def at_offset(t, nbytes):
+    """t's contents in a buffer that starts nbytes behind an allocation's start."""
+    raw = torch.empty(t.numel() * t.element_size() + nbytes, dtype=torch.uint8, device=t.device)
+    out = raw[nbytes:].view(t.dtype).view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@gpu
+def test_bases_at_the_least_alignment(fk):
+    """The same bits from tensors that have only the alignment that the calls ask for."""
+    B, T, H, n, d = 2, 3, 50, 700, 512
+    packed, scales = make_cache(fk, B, n + T, 51)
+    p2, s2 = at_offset(packed, 16), at_offset(scales, 16)
+    lens = torch.tensor([n, 130], dtype=torch.int32, device=DEV)
+    mask = tree_masks(B, T, 3)
+    q = torch.randn(B, T, H, d, generator=gen(52), device=DEV).bfloat16()
+    for idx in (None, torch.randint(0, n, (B, 201), generator=gen(53), device=DEV).int()):
+        out, lse = fk.tree_attn_decode(q, packed, scales, lens, mask, idx=idx, sm_scale=0.04)
+        o2, l2 = fk.tree_attn_decode(at_offset(q, 16), p2, s2, lens, mask, idx=None if idx is None else at_offset(idx, 4),
+                                     sm_scale=0.04, out=at_offset(torch.zeros_like(q), 16), lse=at_offset(lse * 0, 4))
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    rows = torch.randint(-3, B * (n + T) + 3, (333,), generator=gen(54), device=DEV)
+    for dtype, pad in ((torch.bfloat16, 8), (torch.float32, 4)):
+        want = fk.kv_dequant_fp4(packed, scales, src_row=rows, dtype=dtype)
+        wide = at_offset(torch.zeros(333, d + pad, dtype=dtype, device=DEV), 16)
+        got = fk.kv_dequant_fp4(p2, at_offset(scales, 1), src_row=at_offset(rows, 8), out=wide[:, :d])
+        assert torch.equal(got, want) and (wide[:, d:] == 0).all()
+    x = torch.randn(300, d, generator=gen(55), device=DEV).bfloat16()
+    c1, c2 = torch.zeros(300, d // 2, dtype=torch.uint8, device=DEV), torch.zeros(300, d // 16, dtype=torch.uint8, device=DEV)
+    c3, c4 = at_offset(c1, 8), at_offset(c2, 1)
+    fk.qkv_norm_rope_fp4(None, x, packed=c1, scales=c2)
+    fk.qkv_norm_rope_fp4(None, at_offset(x, 16), packed=c3, scales=c4)
+    assert torch.equal(c3, c1) and torch.equal(c4, c2)
+
+
+@gpu
+def test_a_cache_of_more_than_2_gib(fk):
+    """Rows behind 2^31 bytes: written, read back and attended."""
+    cap, d, H, T = 8_500_000, 512, 64, 2
+    packed = torch.zeros(1, cap, d // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(1, cap, d // 16, dtype=torch.uint8, device=DEV)
+    small_p, small_s = make_cache(fk, 1, 300 + T, 56)
+    at = torch.cat([torch.arange(150, device=DEV), torch.arange(cap - T - 150, cap, device=DEV)])
+    packed[0, at], scales[0, at] = small_p[0], small_s[0]
+    x = torch.randn(T, d, generator=gen(57), device=DEV).bfloat16()
+    fk.qkv_norm_rope_fp4(None, x, packed=packed, scales=scales, dst_row=at[-T:].contiguous())
+    fk.qkv_norm_rope_fp4(None, x, packed=small_p, scales=small_s, dst_row=torch.arange(300, 300 + T, device=DEV))
+    assert torch.equal(fk.kv_dequant_fp4(packed, scales, src_row=at), fk.kv_dequant_fp4(small_p, small_s))
+    q = torch.randn(1, T, H, d, generator=gen(58), device=DEV).bfloat16()
+    mask = torch.tensor([[1, 3]], dtype=torch.int64, device=DEV)
+    far = fk.tree_attn_decode(q, packed, scales, torch.tensor([cap - T], dtype=torch.int32, device=DEV), mask,
+                              idx=at[:300].int().view(1, -1), sm_scale=0.04)
+    near = fk.tree_attn_decode(q, small_p, small_s, torch.tensor([300], dtype=torch.int32, device=DEV), mask,
+                               idx=torch.arange(300, dtype=torch.int32, device=DEV).view(1, -1), sm_scale=0.04)
+    assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+
+
+@gpu
+def test_two_streams_at_once_and_nothing_drafted(fk):
+    """Calls with their own workspaces overlap on two streams; a batch without a single draft writes nothing."""
+    B, T, H, n = 2, 4, 64, 3000
+    packed, scales = make_cache(fk, B, n + T, 59)
+    lens = torch.tensor([n, 1700], dtype=torch.int32, device=DEV)
+    mask = tree_masks(B, T, 5)
+    q = [torch.randn(B, T, H, 512, generator=gen(60 + i), device=DEV).bfloat16() for i in range(2)]
+    want = [fk.tree_attn_decode(x, packed, scales, lens, mask, sm_scale=0.04) for x in q]
+    ws = [fk.alloc_workspace(fk.workspace_bytes(fk.OP_TREE_ATTN, B, n + T, T * H, 0), DEV) for _ in q]
+    got = [(torch.zeros_like(o), torch.zeros_like(l)) for o, l in want]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                fk.tree_attn_decode(q[i], packed, scales, lens, mask, sm_scale=0.04, ws=ws[i], out=got[i][0], lse=got[i][1])
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+    o, l = got[0][0].fill_(3.0), got[0][1].fill_(4.0)
+    none = torch.tensor([0, -5], dtype=torch.int32, device=DEV)
+    fk.tree_attn_decode(q[0], packed, scales, lens, mask, n_draft=none, ws=ws[0], out=o, lse=l)
+    assert (o == 3.0).all() and (l == 4.0).all() and all(fk.workspace_status(w) == 0 for w in ws)
