@@ -179,7 +179,7 @@ struct TreeLayout {
 
 // rows: T * H query rows per sequence; top_k 0: every row of the prefix is attended. A cluster
 // leaves at most two unfinished items: the one it begins with and the one it ends with (none where
-// items are not shared).
+// items are shared for no B: a workspace for a large batch serves a smaller one too).
 TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int sms) {
   TreeLayout L;
   L.n_clusters = fp4kv::tree_clusters(B, rows, cap, top_k, sms);
@@ -187,7 +187,7 @@ TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int 
   L.first_tile = off;
   off += up(sizeof(uint32_t) * (B + 2));
   L.part_ml = off;
-  const int64_t parts = fp4kv::tree_whole_items(cap, top_k) ? 0 : 2 * L.n_clusters;
+  const int64_t parts = fp4kv::tree_always_whole(cap, top_k) ? 0 : 2 * L.n_clusters;
   off += up(sizeof(float) * parts * 128 * 2);
   L.part_o = off;
   off += up(sizeof(float) * parts * 128 * 512);
@@ -738,7 +738,7 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.n_clusters = L.n_clusters;
   p.min_tiles = fp4kv::tree_min_tiles();
-  p.whole = fp4kv::tree_whole_items(cap, top_k);
+  p.whole = fp4kv::tree_whole_items(B, int64_t(T) * H, cap, top_k, sms);
   p.first_tile = reinterpret_cast<uint32_t*>(base + L.first_tile);
   p.part_ml = reinterpret_cast<float*>(base + L.part_ml);
   p.part_o = reinterpret_cast<float*>(base + L.part_o);

@@ -157,7 +157,8 @@ struct TreeAttnParams {
 int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k);
 int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms);
 int tree_min_tiles();
-bool tree_whole_items(int64_t cap, int64_t top_k);
+bool tree_always_whole(int64_t cap, int64_t top_k);  // whatever B and rows are
+bool tree_whole_items(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms);
 cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------------------

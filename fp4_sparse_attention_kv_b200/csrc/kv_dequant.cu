@@ -132,9 +132,11 @@ cudaError_t launch_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
                                   const int64_t* src_row, int64_t n_rows, void* out, bool f32, int64_t out_row_stride,
                                   int num_sms, cudaStream_t stream) {
   if (n_rows == 0) return cudaSuccess;
-  // two units per thread where that still fills the GPU, one where latency counts
+  // Two units per thread, whose loads overlap, where one unit each would be more than the threads that fit;
+  // one where latency counts. Gathered rows of 512, one against two units: 16,384 to bf16 6.2 against 6.5 us,
+  // to fp32 8.3 against 6.8, 37,888 to bf16 10.0 against 7.8, 65,536 14.5 against 13.0.
   const int64_t units = n_rows * (d / (f32 ? 16 : 32));
-  const bool big = units >= int64_t(num_sms) * 8 * kThreads * 2;
+  const bool big = units > int64_t(num_sms) * 8 * kThreads;
   if (f32)
     return big ? launch<true, 2>(packed, scales, cap_rows, d, src_row, n_rows, out, out_row_stride, stream)
                : launch<true, 1>(packed, scales, cap_rows, d, src_row, n_rows, out, out_row_stride, stream);

@@ -457,8 +457,10 @@ FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
   }
 }
 
-// Rows of a KV warp: eight (four of more than 512 channels), whose rotated groups share the lanes; where
-// there are too few for every SM, as few as a pass has.
+// Rows of a KV warp: eight (four of more than 512 channels), whose rotated groups share the lanes and whose
+// loads overlap; where that leaves SMs without a warp or two, as few as a pass has. Rows of 512, one pass
+// against eight: 1,024 rows 8.3 against 9.0 us, 4,096 10.6 against 9.2, 9,472 16.5 against 10.1, 131,072 170
+// against 93.
 template <int LPR, int GPL>
 constexpr int kKvPasses = (GPL == 1 ? 8 : 4) * LPR / 32;
 
@@ -487,13 +489,16 @@ __global__ void __launch_bounds__(kThreads, GPL == 1 ? 2 : 1) k_qkv_norm_rope(co
   query_heads<LPR, GPL, kPairs>(p, smem_u32(ring[threadIdx.x >> 5]), tok, h0, min(h0 + heads, p.H));
 }
 
+// (what takes the GPU no longer than the host is launched plainly)
+bool few_rows(int64_t rows, int num_sms) { return rows < int64_t(num_sms) * 64; }
+
 template <int LPR, int GPL, int kPairs, int kPasses>
-cudaError_t launch_kv(const NormRopeParams& p, cudaStream_t stream) {
+cudaError_t launch_kv(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t per_block = kPasses * (32 / LPR) * (kThreads / 32);
   const int64_t blocks = (p.n_tokens + per_block - 1) / per_block;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_sized(kPasses == 1, k_kv_norm_rope<LPR, GPL, kPairs, kPasses>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
-                      stream, p);
+  return launch_sized(few_rows(p.n_tokens, num_sms), k_kv_norm_rope<LPR, GPL, kPairs, kPasses>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kThreads), stream, p);
 }
 
 template <int LPR, int GPL, int kPairs>
@@ -503,17 +508,19 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t kv_blocks = p.kv ? (p.n_tokens + per_block - 1) / per_block : 0;
   if (!p.q) {
     constexpr int kMany = kKvPasses<LPR, GPL>;
-    return p.n_tokens >= int64_t(num_sms) * 16 * kMany * kRows ? launch_kv<LPR, GPL, kPairs, kMany>(p, stream)
-                                                               : launch_kv<LPR, GPL, kPairs, 1>(p, stream);
+    return p.n_tokens >= int64_t(num_sms) * 2 * kMany * kRows ? launch_kv<LPR, GPL, kPairs, kMany>(p, num_sms, stream)
+                                                              : launch_kv<LPR, GPL, kPairs, 1>(p, num_sms, stream);
   }
-  // heads per warp: one pass (kRows) where there are few rows, up to 16 passes where that leaves every SM
-  // 32 warps to run
+  // Heads per warp: one pass (kRows) where there are few rows, up to 16 passes where that leaves every SM
+  // 8 warps (as many as its ring of rows needs, and the coefficients are formed once for all of them). 64
+  // heads of 512, 1, 4 and 16 a warp: 32 tokens 8.3, 7.6, 8.0 us (the host's time), 128 tokens 10.4, 7.5, 8.2, 512
+  // tokens 30.8, 14.5, 11.6, 8,192 tokens 507, 222, 166.
   int heads = kRows;
-  while (heads < 16 * kRows && heads < p.H && p.n_tokens * p.H >= int64_t(2) * heads * 32 * num_sms) heads *= 2;
+  while (heads < 16 * kRows && heads < p.H && p.n_tokens * p.H >= int64_t(2) * heads * 8 * num_sms) heads *= 2;
   const int64_t units = p.n_tokens * ((p.H + heads - 1) / heads);
   const int64_t blocks = kv_blocks + (units + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_sized(heads == kRows, k_qkv_norm_rope<LPR, GPL, kPairs>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), stream,
+  return launch_sized(few_rows(p.n_tokens * (p.H + 1) / kRows, num_sms), k_qkv_norm_rope<LPR, GPL, kPairs>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), stream,
                       p, static_cast<uint32_t>(kv_blocks), heads);
 }
 

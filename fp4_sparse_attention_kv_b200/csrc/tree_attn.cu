@@ -234,8 +234,9 @@ FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
 // All tile counts fit 32 bits (the host refuses more): a 64-bit division is a call of 100 instructions.
 // Clusters in use for `total` tiles of `items` items, whose tiles are `tiles` each (0: not all the same):
 // at least min_tiles each. Where whole fractions of an item to a cluster cost no more than the parts
-// that begin and end anywhere, they are taken: a cluster then has one segment, not two. A segment
-// costs about as much as 8 tiles (Q, the pipeline's start, the output: 18,000 of 2,300 cycles).
+// that begin and end anywhere, they are taken: a cluster then has one segment, not two, and a segment costs
+// about as much as 8 tiles (Q, the pipeline's start, the output). With fractions and without: 32 items of 33
+// tiles 42.1 and 46.3 us, 16 of 63 41.0 and 44.3, 32 of 63 58.4 and 59.4, 8 of 313 66.1 and 70.2.
 FP4KV_DEV uint32_t clusters_used(uint32_t total, uint32_t items, uint32_t tiles, uint32_t n_clusters, uint32_t min_tiles) {
   const uint32_t n = max(1u, min(n_clusters, total / min_tiles + (total % min_tiles != 0)));
   if (tiles == 0 || items > n) return n;
@@ -1021,16 +1022,30 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
 
 int tree_min_tiles() { return 2; }
 
-// Items of few tiles are not shared between clusters: up to 10 tiles, the parts' way through the
-// workspace and the second launch cost as much as the tiles that are saved.
-bool tree_whole_items(int64_t cap, int64_t top_k) { return ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile <= 10; }
+// Items go whole to a cluster where sharing them would save less than it costs. A segment costs what
+// kSegment tiles do beside its own, so whole items take ceil(items / clusters) (tiles + kSegment); sharing
+// levels that to items / clusters, for one more segment per cluster and the second launch: 17 tiles together.
+// Items of more than 20 tiles are always shared (their real lengths, which the host doesn't know, may
+// differ). 64 heads, whole against shared: 4 items of 8 tiles 22.5 against 22.8 us, of 15 30.9 against
+// 25.0; 16 items of 5 19.8 against 23.8; 96 items of 9 42.0 against 51.0, of 15 55.8 against 61.1, of 22 72.6
+// against 71.1; 128 items of 8 40.5 against 58.4.
+constexpr int64_t kSegment = 8, kSharing = 17, kMostWhole = 20;
+static int64_t tree_item_tiles(int64_t cap, int64_t top_k) { return ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile; }
+
+bool tree_always_whole(int64_t cap, int64_t top_k) { return tree_item_tiles(cap, top_k) + kSegment <= kSharing; }
+
+bool tree_whole_items(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms) {
+  const int64_t t = tree_item_tiles(cap, top_k), items = B * ((rows + kRows - 1) / kRows), most = num_sms / 2;
+  const int64_t idle = (most - items % most) % most;  // clusters without an item in the last turn
+  return tree_always_whole(cap, top_k) || (t <= kMostWhole && idle * (t + kSegment) <= kSharing * most);
+}
 
 int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k) {
-  return B * ((rows + kRows - 1) / kRows) * (((top_k ? top_k : cap) + 64 + kTile - 1) / kTile);
+  return B * ((rows + kRows - 1) / kRows) * tree_item_tiles(cap, top_k);
 }
 
 int tree_clusters(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms) {
-  const int64_t most = tree_whole_items(cap, top_k)
+  const int64_t most = tree_always_whole(cap, top_k)
                            ? B * ((rows + kRows - 1) / kRows)
                            : (tree_tiles(B, rows, cap, top_k) + tree_min_tiles() - 1) / tree_min_tiles();
   return static_cast<int>(most < num_sms / 2 ? most : num_sms / 2);

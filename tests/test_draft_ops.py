@@ -214,6 +214,13 @@ def test_tree_workspace_sizes():
     assert wb(binding.OP_TREE_ATTN, 1, 100, 8, 0) <= wb(binding.OP_TREE_ATTN, 1, 100000, 8 * 64, 0)
 
 
+@pytest.mark.parametrize("cap, top_k", [(100, 0), (512, 0), (600, 0), (1000, 0), (1300, 0), (70000, 0), (70000, 512), (70000, 800)])
+def test_a_tree_workspace_for_a_batch_serves_every_smaller_one(cap, top_k):
+    sizes = [binding.workspace_bytes(binding.OP_TREE_ATTN, B, cap, rows, top_k) for rows in (8, 128, 500) for B in range(1, 160)]
+    for at in range(0, len(sizes), 159):
+        assert sizes[at:at + 159] == sorted(sizes[at:at + 159])
+
+
 def test_binding_refuses_cpu_tensors_and_missing_arguments():
     x = torch.zeros(2, 512, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
@@ -746,6 +753,39 @@ def at_offset(t, nbytes):
     out = raw[nbytes:].view(t.dtype).view(t.shape)
     out.copy_(t)
     return out
+
+
+@gpu
+@pytest.mark.parametrize("B, T, H, cap", [(8, 9, 64, 700), (74, 2, 64, 800), (75, 2, 64, 800), (72, 1, 5, 1100), (37, 4, 64, 1216), (37, 4, 64, 1217)])
+def test_tree_batches_on_either_side_of_the_sharing_rule(fk, B, T, H, cap):
+    """Items whole or shared by how evenly they fill the GPU, with lengths that differ widely."""
+    lens = [(cap - T) * ((5 * b) % 9) // 8 for b in range(B)]
+    run_tree(fk, B, T, H, lens, [T - b % (T + 1) for b in range(B)], cap, seed=13)
+
+
+@gpu
+@pytest.mark.parametrize("n, H, d, rope, half", [(2367, 0, 512, 64, True), (2368, 0, 512, 64, False), (2368, 0, 1024, 64, False), (4800, 0, 128, 64, True),
+                                                 (37, 128, 64, 32, False), (150, 63, 512, 64, True), (300, 64, 96, 0, False), (297, 33, 256, 256, False)])
+def test_norm_rope_on_either_side_of_its_splits(fk, n, H, d, rope, half):
+    g = gen(n + d)
+    kv = torch.randn(n, d, generator=g, device=DEV).bfloat16()
+    q = torch.randn(n, H, d, generator=g, device=DEV).bfloat16() if H else None
+    table, pos = table_of(100, rope) if rope else None, torch.arange(n, device=DEV) % 100
+    qo, ko = fk.qkv_norm_rope_fp4(q, kv, positions=pos if rope else None, cos_sin=table, rope_dim=rope, rope_half=half)
+    if H:
+        check_q(qo, q, None, pos, table, rope, half, 1e-6)
+    assert torch.equal(ko, bf16_of_f64(plain_norm_rope(kv, None, pos, table, rope, half, 1e-6)[0]))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [9471, 9473, 18944, 18945])
+def test_dequant_on_either_side_of_its_split(fk, n, dtype):
+    packed, scales = make_cache(fk, 1, 900, 14)
+    rows = torch.randint(-1, 901, (n,), generator=gen(n), device=DEV)
+    v = cache_values(packed[0], scales[0]).to(DEV)
+    want = torch.where(((rows >= 0) & (rows < 900))[:, None], v[rows.clamp(0, 899)], 0.0)
+    assert torch.equal(fk.kv_dequant_fp4(packed, scales, src_row=rows, dtype=dtype).double(), want)
 
 
 @gpu
