@@ -862,3 +862,69 @@ def test_two_streams_at_once_and_nothing_drafted(fk):
     none = torch.tensor([0, -5], dtype=torch.int32, device=DEV)
     fk.tree_attn_decode(q[0], packed, scales, lens, mask, n_draft=none, ws=ws[0], out=o, lse=l)
     assert (o == 3.0).all() and (l == 4.0).all() and all(fk.workspace_status(w) == 0 for w in ws)
+
+
+@gpu
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("n, H, d", [(520, 64, 512), (2400, 0, 512), (2400, 0, 128), (2400, 0, 1024), (3, 64, 512)])
+def test_norm_rope_in_place_at_every_split(fk, n, H, d, half):
+    """Rows written over themselves give the bits of separate outputs."""
+    q = torch.randn(n, H, d, generator=gen(81), device=DEV).bfloat16() if H else None
+    kv = torch.randn(n, d, generator=gen(82), device=DEV).bfloat16()
+    table, pos = table_of(50, 64), torch.arange(n, device=DEV) % 50
+    how = dict(positions=pos, cos_sin=table, rope_dim=64, rope_half=half)
+    qw, kw = fk.qkv_norm_rope_fp4(q, kv, **how)
+    qo, ko = fk.qkv_norm_rope_fp4(q, kv, q_out=q, kv_out=kv, **how)
+    assert torch.equal(ko, kw) and ko.data_ptr() == kv.data_ptr()
+    assert H == 0 or (torch.equal(qo, qw) and qo.data_ptr() == q.data_ptr())
+
+
+@gpu
+@pytest.mark.parametrize("B, T, n", [(2, 4, 300), (16, 16, 1500)])  # (plain launches and whole items; dependent ones and a merge)
+def test_a_captured_step_replays_with_what_the_tensors_hold_then(fk, B, T, n):
+    """Norm and write, tree, read-back in one graph: replayed after every input has changed, equal to the calls
+    made one by one."""
+    H, d, rope, cap = 64, 512, 64, n + T
+    table = table_of(cap, rope)
+    ws = fk.alloc_workspace(fk.workspace_bytes(fk.OP_TREE_ATTN, B, cap, T * H, 0), DEV)
+    packed, scales = make_cache(fk, B, cap, 83)
+    x = torch.empty(B * T, (H + 1) * d, dtype=torch.bfloat16, device=DEV)
+    lens, mask = torch.empty(B, dtype=torch.int32, device=DEV), torch.empty(B, T, dtype=torch.int64, device=DEV)
+    pos, dst = torch.empty(B * T, dtype=torch.int64, device=DEV), torch.empty(B * T, dtype=torch.int64, device=DEV)
+    q = torch.empty(B, T, H, d, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(B, T, H, device=DEV)
+    rows = torch.empty(B * T, d, dtype=torch.bfloat16, device=DEV)
+
+    def fill(seed):
+        x.copy_(torch.randn(x.shape, generator=gen(seed), device=DEV))
+        lens.copy_(torch.randint(0, n + 1, (B,), generator=gen(seed + 1), device=DEV))
+        mask.copy_(tree_masks(B, T, seed))
+        pos.copy_((lens.long()[:, None] + torch.arange(T, device=DEV)).view(-1))
+        dst.copy_(pos + torch.arange(B, device=DEV).repeat_interleave(T) * cap)
+
+    def step():
+        fk.qkv_norm_rope_fp4(x[:, : H * d].view(B * T, H, d), x[:, H * d:], positions=pos, cos_sin=table, rope_dim=rope,
+                             packed=packed, scales=scales, dst_row=dst, q_out=q.view(B * T, H, d))
+        fk.tree_attn_decode(q, packed, scales, lens, mask, sm_scale=0.04, ws=ws, out=out, lse=lse)
+        fk.kv_dequant_fp4(packed, scales, src_row=dst, out=rows)
+
+    fill(90)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (91, 95):
+        fill(seed)
+        keep = packed.clone(), scales.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (q, out, lse, rows, packed, scales)]
+        packed.copy_(keep[0]), scales.copy_(keep[1])
+        for t in (q, out, lse, rows):
+            t.zero_()
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (q, out, lse, rows, packed, scales)):
+            assert torch.equal(a, b)
+    assert fk.workspace_status(ws) == 0
