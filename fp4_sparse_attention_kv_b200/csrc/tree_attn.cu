@@ -22,7 +22,7 @@
 //
 // A CTA (28 warps):
 //  * warps 16-23 dequantize a tile's 64 rows to fp16 (exact) in 128-byte-swizzled 64-channel chunks,
-//    the K-major B operand of S and the MN-major B operand of O; loads run two tiles ahead;
+//    the K-major B operand of S and the MN-major B operand of O; loads run a tile ahead;
 //  * warp 24 issues the MMAs: S(t) with A = Q in TMEM, or O += P(t) V(t) with A = P in shared memory;
 //  * warps 0-15 own TMEM lane quarter w % 4 (query rows); warps 0-7 work on the even tiles, 8-15 on
 //    the odd ones. Scores: reference and sum in registers (lane = query row, 32 columns a thread);
@@ -536,7 +536,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         const uint32_t e = (it.tile0 + i) * kTile + row;
         return i < it.nt && idx && e < s.n_sel ? idx[e] : static_cast<int32_t>(e);
       };
-      auto load = [&](RawRow& r, uint32_t i, int32_t ent) {
+      // Where this thread's row of tile i lies (-1: absent), and a chunk of it.
+      auto place = [&](uint32_t i, int32_t ent) -> int64_t {
         const uint32_t e = (it.tile0 + i) * kTile + row;
         int64_t pos = static_cast<uint32_t>(ent);
         bool there = i < it.nt;
@@ -547,55 +548,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           pos = int64_t(s.pre) + d;
           there = there && d < uint32_t(s.nd) && ((seen >> d) & 1) && pos < p.cap;
         }
-        if (there) {
-          const uint8_t* c = packed + pos * (kD / 2);
-          const uint8_t* f = scales + pos * (kD / kGroup);
-          ld_nc_32b(r.c[0], c, al32);
-          ld_nc_32b(r.c[1], c + 128, al32);
-          r.s[0] = *reinterpret_cast<const uint32_t*>(f);
-          r.s[1] = *reinterpret_cast<const uint32_t*>(f + 16);
+        return there ? pos : -1;
+      };
+      auto load = [&](uint32_t (&c)[8], uint32_t& sc, int64_t pos, int k) {
+        if (pos >= 0) {
+          ld_nc_32b(c, packed + pos * (kD / 2) + 128 * k, al32);
+          sc = *reinterpret_cast<const uint32_t*>(scales + pos * (kD / kGroup) + 16 * k);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) r.c[0][k] = r.c[1][k] = 0;
-          r.s[0] = r.s[1] = 0;
+          for (int u = 0; u < 8; ++u) c[u] = 0;
+          sc = 0;
         }
       };
-      const int32_t e0 = entry(0), e1 = entry(1);
-      int32_t ent = entry(2);
+      const int32_t e0 = entry(0);
+      int32_t ent = entry(1);
       seen = uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen))) |
              (uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen >> 32))) << 32);
-      RawRow ra, rb;  // tiles i and i + 1 (each reloaded in place: a copy would wait for its loads)
-      load(ra, 0, e0);
-      load(rb, 1, e1);
+      // The next tile's, loaded over the one that has just been converted. (Two tiles ahead in two buffers, the loop
+      // is written out twice: fetching its instructions costs more than the loads' latency, 302 against 280 us for
+      // 4 x 1,024 query rows over 32,784; once more per kind of CTA 368, a loop over the two chunks 348.)
+      RawRow r;
+      {
+        const int64_t pos = place(0, e0);
+        load(r.c[0], r.s[0], pos, 0);
+        load(r.c[1], r.s[1], pos, 1);
+      }
       if (seg == 0) join();
       // (Q comes through the stages, but for a first item of up to 64 rows: then this wait comes at the end)
       const bool q_apart = seg == 0 && s.nd * p.H - static_cast<int>(it.g) * kRows <= 64;
       if (!values && !q_apart) ok = ok && !aborted() && warp_wait(&bars[B_QREADY], seg & 1);
-      auto tile = [&](RawRow& r, uint32_t i) {
-        if (!ok || i >= it.nt) return;
+      for (uint32_t i = 0; ok && i < it.nt; ++i) {
         // (eight warps that wait most of the time: sparing polls leave shared memory to the others)
         ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&bars[B_VFREE + 2 * st + half], sph ^ 1, 32));
-        if (!ok) return;
+        if (!ok) break;
         const uint32_t at = unit0 + st * kVBytes;
         // A row with a NaN scale makes its logits NaN, so p is NaN for those who see it and 0 for the others; as a
-        // value it is read as finite, since 0 * NaN would reach the others too. (As the value CTA
-        // waits most of the time, this costs least here: 295 to 301 us for 4 x 1,024 query rows over 32,784.)
+        // value it is read as finite, since 0 * NaN would reach the others too.
         if (values) {
           r.s[0] = finite_scales(r.s[0]);
           r.s[1] = finite_scales(r.s[1]);
         }
         dequant_chunk(at, j, r.c[0], r.s[0]);
         dequant_chunk(at + 4 * kVChunk, j, r.c[1], r.s[1]);
+        const int64_t pos = place(i + 1, ent);
+        load(r.c[0], r.s[0], pos, 0);
+        load(r.c[1], r.s[1], pos, 1);
+        ent = entry(i + 2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_VFULL + 2 * st + half]);
-        load(r, i + 2, ent);
-        ent = entry(i + 3);
         next_stage();
-      };
-      for (uint32_t i = 0; ok && i < it.nt; i += 2) {
-        tile(ra, i);
-        tile(rb, i + 1);
       }
       if (!values && q_apart) ok = ok && warp_wait(&bars[B_QREADY], seg & 1);
       if (!ok) give_up();
