@@ -15,10 +15,10 @@
 // made, 16 KiB a tile, in one direction only: no round trip is on the path of a tile, and each CTA's
 // tensor work is the same, 1,024 cycles a tile. Both dequantize the tile's rows for themselves.
 // (Splitting the channels instead, each CTA with half of q, V and O, needs S summed over the two CTAs:
-// 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile; this one takes about 2,600.)
-// 4 x 1,024 query rows over 32,784 rows each: 305 us, 902 TFLOP/s, the tensor pipe 46 % active; bound by the
-// scoring CTA's dequantization (1,150 cycles a tile) beside its softmax. 8 x 512 over 2,056: 44 us, 32 x 320
-// over 517: 39 us, bound by an item's start and end.
+// 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile; this one takes about 2,400.)
+// 4 x 1,024 query rows over 32,784 rows each: 291 us, 946 TFLOP/s, the tensor pipe 50 % active; bound by the
+// scoring CTA's dequantization beside its softmax (instruction fetch, and the L1 data pipe's 1,670 wavefronts a
+// tile). 8 x 512 over 2,056: 42 us, 32 x 320 over 517: 37 us, bound by an item's start and end.
 //
 // A CTA (28 warps):
 //  * warps 16-23 dequantize a tile's 64 rows to fp16 (exact) in 128-byte-swizzled 64-channel chunks,
