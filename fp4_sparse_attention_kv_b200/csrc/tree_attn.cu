@@ -17,8 +17,8 @@
 // (Splitting the channels instead, each CTA with half of q, V and O, needs S summed over the two CTAs:
 // 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile; this one takes about 2,400.)
 // 4 x 1,024 query rows over 32,784 rows each: 291 us, 946 TFLOP/s, the tensor pipe 50 % active; bound by the
-// scoring CTA's dequantization beside its softmax (instruction fetch, and the L1 data pipe's 1,670 wavefronts a
-// tile). 8 x 512 over 2,056: 42 us, 32 x 320 over 517: 37 us, bound by an item's start and end.
+// scoring CTA's dequantization beside its softmax (the L1 data pipe carries 1,670 wavefronts a tile, issue slots are
+// 54 % busy). 8 x 512 over 2,056: 42 us, 32 x 320 over 517: 37 us, bound by an item's start and end.
 //
 // A CTA (28 warps):
 //  * warps 16-23 dequantize a tile's 64 rows to fp16 (exact) in 128-byte-swizzled 64-channel chunks,
@@ -564,9 +564,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
       int32_t ent = entry(1);
       seen = uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen))) |
              (uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(seen >> 32))) << 32);
-      // The next tile's, loaded over the one that has just been converted. (Two tiles ahead in two buffers, the loop
-      // is written out twice: fetching its instructions costs more than the loads' latency, 302 against 280 us for
-      // 4 x 1,024 query rows over 32,784; once more per kind of CTA 368, a loop over the two chunks 348.)
+      // The next tile's, loaded over the one that has just been converted. (Two tiles ahead
+      // in two buffers, the loop written out twice, took 302 against 280 us for 4 x 1,024 query rows over 32,784:
+      // 3 % more instructions, 53 times the spill stores, and more waiting for instructions. Written out once more,
+      // for either kind of CTA: 368, with 6 times that waiting. A loop over the two chunks: 348.)
       RawRow r;
       {
         const int64_t pos = place(0, e0);
