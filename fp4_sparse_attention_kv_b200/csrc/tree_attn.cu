@@ -11,14 +11,15 @@
 // it leaves (O, reference, sum) in the workspace and k_tree_merge joins them in a fixed order.
 //
 // Split in a cluster: O of 128 x 512 in fp32 is all of an SM's TMEM, so one CTA makes S = Q V^T and the
-// softmax (Q in TMEM, four slots of S beside it) and the other one O += P V. P goes over as it is
-// made, 16 KiB a tile, in one direction only: no round trip is on the path of a tile, and each CTA's
-// tensor work is the same, 1,024 cycles a tile. Both dequantize the tile's rows for themselves.
+// softmax (Q in TMEM, four slots of S beside it) and the other one O += P V, with P in two parts of fp16. P goes
+// over as it is made, 32 KiB a tile, in one direction only: no round trip is on the path of a tile. Both
+// dequantize the tile's rows for themselves. Tensor work is 1,024 cycles a tile for the scores, 2,048 for the values.
 // (Splitting the channels instead, each CTA with half of q, V and O, needs S summed over the two CTAs:
-// 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile; this one takes about 2,400.)
-// 4 x 1,024 query rows over 32,784 rows each: 291 us, 946 TFLOP/s, the tensor pipe 50 % active; bound by the
-// scoring CTA's dequantization beside its softmax (the L1 data pipe carries 1,670 wavefronts a tile, issue slots are
-// 54 % busy). 8 x 512 over 2,056: 42 us, 32 x 320 over 517: 37 us, bound by an item's start and end.
+// 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile, with P in one part. P in one part took
+// 2,030 cycles a tile in this form, in two it takes 2,370.)
+// 4 x 1,024 query rows over 32,784 rows each: 340 us, bound by the values' tensor work (86 % of a tile's cycles, at
+// the 1.6 GHz that the power limit leaves). 8 x 512 over 2,056: 52 us, 32 x 320 over 517: 46 us, bound by an item's
+// start and end.
 //
 // A CTA (28 warps):
 //  * warps 16-23 dequantize a tile's 64 rows to fp16 (exact) in 128-byte-swizzled 64-channel chunks,
@@ -29,8 +30,10 @@
 //    the reference is handed from set to set. Values: P's arrival, O's rescaling, the output.
 // Numerics: q as fp16 times a power of two per row (exact down to 2^-28 of the row's maximum), v exact
 // in fp16, S and O in fp32. The reference m moves only when a logit passes it by 2^9 (log2 domain),
-// to 2^3 above the maximum; p is stored as p * 2^6 in fp16, so the row's largest is at least 2^3 and at
-// most 2^15: 11 bits each, and below 2^-14 a step of 2^-24, 2^-27 of the largest. The sums are fp32.
+// to 2^-1 of the maximum; p is made as p * 2^6, so the row's largest is at least 2^7 and at most 2^15, and goes as two
+// fp16: its upper 11 bits and the rest, rounded to 11 bits. Together they are off by at most 2^-21 of p, or by
+// 2^-24, 2^-31 of the largest. One fp16 alone, 2^-12, would show where rows cancel, and breaks the library's
+// bound on its attention (5e-3 in every value) where some rows are a hundred times louder. The sums are fp32.
 // Every wait is bounded; on timeout a status bit is set and the kernel winds down.
 #include <atomic>
 
@@ -49,33 +52,35 @@ constexpr int kCols = kTile / 2;  // columns of S per softmax warp
 constexpr int kSoftWarps = 16, kDeqWarps = 8, kMmaWarp = 24;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole warpgroups: registers move between them)
 constexpr int kStages = 2;  // tiles of V
-constexpr int kSlots = 4;                          // tiles of S and of P
+constexpr int kSlots = 4;   // tiles of S
+constexpr int kPSlots = 2;  // tiles of P: tile m's in slot m & 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMoveLog2 = 9.0f, kHeadroomLog2 = 3.0f, kPLog2 = 6.0f;
+constexpr float kMoveLog2 = 9.0f, kHeadroomLog2 = -1.0f, kPLog2 = 6.0f;  // (in the log2 domain)
 
 constexpr uint32_t kVChunk = kTile * 128;         // [64 rows][64 channels]
 constexpr uint32_t kVBytes = 8 * kVChunk;         // 64 KiB
-constexpr uint32_t kPBytes = kRows * 128;         // [2 column halves][128 query rows][64 B] fp16
+constexpr uint32_t kPHalf = kRows * 128;          // [16 groups of 8 query rows][high, low part][8][64 B] fp16
+constexpr uint32_t kPBytes = 2 * kPHalf;          // two halves of 32 columns
 constexpr uint32_t kOffV = 0;                     // (scores: first Q's way into TMEM)
-constexpr uint32_t kOffP = kOffV + kStages * kVBytes;  // 4 slots: as it is made, and as it arrives
-constexpr uint32_t kOffBar = kOffP + kSlots * kPBytes;
+constexpr uint32_t kOffP = kOffV + kStages * kVBytes;  // slots of P: as it is made, and as it arrives
+constexpr uint32_t kOffBar = kOffP + kPSlots * kPBytes;
 constexpr uint32_t kOffMisc = kOffBar + 320;
 constexpr uint32_t kOffIter = kOffBar + 336;      // the cluster's range (a SegIter)
 constexpr uint32_t kOffC = kOffBar + 448;         // scores: [128] power of two of the query rows
 constexpr uint32_t kOffPair = kOffC + 512;        // scores: [4][128] exchange between a row's four threads
 constexpr uint32_t kOffRef = kOffPair + 2048;     // scores: [2][128] reference after the last tile of either parity
-constexpr uint32_t kOffA = kOffRef + 1024;        // values: [4 slots][128] factors of O
-constexpr uint32_t kOffML = kOffA + 2048;         // values: [4 slots][2][128] reference and sum, with an item's last tile
-constexpr uint32_t kSmem = kOffML + 4096;
+constexpr uint32_t kOffA = kOffRef + 1024;        // values: [2 slots][128] factors of O
+constexpr uint32_t kOffML = kOffA + 1024;         // values: [2 slots][2][128] reference and sum, with an item's last tile
+constexpr uint32_t kSmem = kOffML + 2048;
 static_assert(kSmem <= 232448, "shared memory");
 
 // TMEM columns. Scores: Q [0, 256), S slots [256, 512). Values: O [0, 512).
 constexpr uint32_t kColS = 256;
 
-// Barriers. V's have two halves of 32 rows. Of the slots: SFULL, SFREE (scores), PXFULL, PREADY (values) and PFREE
-// (O has the slot's P, in both). SEG: the last product of an item is complete. A wait goes by parity, so nobody may
+// Barriers. V's have two halves of 32 rows. Of S's slots: SFULL, SFREE (scores). Of P's: PXFULL, PREADY (values) and,
+// for either half, PFREE (O has it, in both). SEG: the last product of an item is complete. A wait goes by parity, so nobody may
 // wait for a use of a barrier before the use before it is known to be over.
-enum { B_VFULL = 0, B_VFREE = 6, B_SFULL = 12, B_SFREE = 16, B_PFREE = 20, B_PXFULL = 24, B_PREADY = 28, B_REF = 32,
+enum { B_VFULL = 0, B_VFREE = 6, B_SFULL = 12, B_SFREE = 16, B_PFREE = 20, B_PXFULL = 24, B_PREADY = 26, B_REF = 32,
        B_QREADY = 34, B_SEG = 35, B_DONE = 36, B_COUNT = 37 };
 static_assert(8 * B_COUNT <= 320, "barriers");
 
@@ -176,8 +181,8 @@ FP4KV_DEV void umma_ss(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t
       " setp.ne.b32 g, %5, 0;\n @g tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}"
       ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go), "n"(kAHigh), "n"(kBHigh) : "memory");
 }
-// High words of the 128-byte and 64-byte swizzled layouts: 1024 or 512 bytes between 8-row groups.
-constexpr uint32_t kHigh128 = (1024u >> 4) | (1u << 14) | (2u << 29), kHigh64 = (512u >> 4) | (1u << 14) | (4u << 29);
+// High words of the 128-byte and 64-byte swizzled layouts: 1024 bytes between 8-row groups (P's high and low parts alternate).
+constexpr uint32_t kHigh128 = (1024u >> 4) | (1u << 14) | (2u << 29), kHigh64 = (1024u >> 4) | (1u << 14) | (4u << 29);
 FP4KV_DEV void commit_if(uint32_t go, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred g;\n setp.ne.b32 g, %1, 0;\n"
@@ -466,7 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars[B_SFULL + i], 1);
       mbar_init(&bars[B_SFREE + i], kSoftWarps / 2);
-      mbar_init(&bars[B_PFREE + i], 1);
+    }
+    for (int i = 0; i < 2 * kPSlots; ++i) mbar_init(&bars[B_PFREE + i], 1);
+    for (int i = 0; i < kPSlots; ++i) {
       mbar_init(&bars[B_PXFULL + i], 1);
       mbar_init(&bars[B_PREADY + i], kSoftWarps / 2);
     }
@@ -641,25 +648,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           const uint32_t dv = static_cast<uint32_t>(sw128_mnmajor_desc(smem_u32(smem + kOffV), kVChunk));
           const uint32_t dp = static_cast<uint32_t>(sw64_kmajor_desc(smem_u32(smem + kOffP)));
           for (uint32_t i = 0; ok && i < it.nt; ++i) {
-            const uint32_t m = n + i, sl = m & (kSlots - 1);
-            ok = warp_wait(&bars[B_PREADY + sl], (m >> 2) & 1);
+            const uint32_t m = n + i, ps = m & 1;
+            ok = warp_wait(&bars[B_PREADY + ps], (m >> 1) & 1);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {  // 32 cache rows: two steps of 16, two halves of the channels
               ok = ok && warp_wait(&bars[B_VFULL + 2 * st + hf], sph);
               if (ok) {
                 tc_fence_after();
-                const uint32_t a0 = dp + ((sl * kPBytes + hf * (kPBytes / 2)) >> 4);
+                const uint32_t a0 = dp + ((ps * kPBytes + hf * kPHalf) >> 4);
                 const uint32_t b0 = dv + ((st * kVBytes + hf * 4096) >> 4);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                   for (int c = 0; c < 2; ++c)
-                    umma_ss<kHigh64, kHigh128>(go, tm + 256 * c, a0 + 2 * k, b0 + ((2048 * k + 4 * c * kVChunk) >> 4), kIdesc, i > 0 || (hf | k) != 0);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                      umma_ss<kHigh64, kHigh128>(go, tm + 256 * c, a0 + 2 * k + 32 * part, b0 + ((2048 * k + 4 * c * kVChunk) >> 4), kIdesc,
+                                                 i > 0 || (hf | k | part) != 0);
                 commit_if(go, &bars[B_VFREE + 2 * st + hf]);
+                // (an item's last slot is given back after its reference and sum have been read)
+                commit_to_if(go, &bars[B_PFREE + 2 * ps + hf], i + 1 < it.nt ? 3 : 2);
               }
             }
-            // (an item's last slot is given back after its reference and sum have been read)
-            if (ok) commit_to_if(go, &bars[B_PFREE + sl], i + 1 < it.nt ? 3 : 2);
             if (ok && i + 1 == it.nt) commit_if(go, &bars[B_SEG]);
             next_stage();
           }
@@ -826,29 +836,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             l2 = fma2(l2, pack2(f, f), 0);
             ref = to;
           }
-          dead = dead || !warp_wait_cluster(&bars[B_PFREE + sl], ph ^ 1);
-          const uint32_t px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + sl);
-          if (h == 0) st_async_f32(peer_smem + kOffA + 4 * (128 * sl + R), a, px_bar);
-          const uint32_t pw = kOffP + sl * kPBytes + h * (kPBytes / 2) + 32 * q * 64;  // this warp's 2 KiB
-          uint8_t* prow = smem + pw + lane * 64;
           const float m6 = ref == -INFINITY ? -INFINITY : kPLog2 - ref;
-          const uint64_t m62 = pack2(m6, m6);
+          const uint64_t m62 = pack2(m6, m6), kMinus1 = pack2(-1.0f, -1.0f);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
+          for (int u = 0; u < 4; ++u) {  // eight columns: their high parts, then their low parts, in the scores' place
+            uint32_t w[4], v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float z0, z1;
               unpack2(fma2(pack2(__uint_as_float(r[8 * u + 2 * k]), __uint_as_float(r[8 * u + 2 * k + 1])), c2, m62), z0, z1);
               const float e0 = ex2(z0), e1 = ex2(z1);
               l2 = add2(l2, pack2(e0, e1));
-              w[k] = pack_f16x2(e0, e1);
+              // the high part's 11 bits by truncation, so that the rest is exact
+              const float t0 = __uint_as_float(__float_as_uint(e0) & 0xffffe000u), t1 = __uint_as_float(__float_as_uint(e1) & 0xffffe000u);
+              w[k] = pack_f16x2(t0, t1);
+              float d0, d1;
+              unpack2(fma2(pack2(t0, t1), kMinus1, pack2(e0, e1)), d0, d1);
+              v[k] = pack_f16x2(d0, d1);
             }
-            *reinterpret_cast<uint4*>(prow + ((u ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              r[8 * u + k] = w[k];
+              r[8 * u + 4 + k] = v[k];
+            }
+          }
+          // (the slot of this set's tiles)
+          dead = dead || !warp_wait_cluster(&bars[B_PFREE + 2 * set + h], ((m >> 1) & 1) ^ 1);
+          const uint32_t px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + set);
+          if (h == 0) st_async_f32(peer_smem + kOffA + 4 * (128 * set + R), a, px_bar);
+          const uint32_t pw = kOffP + set * kPBytes + h * kPHalf + q * (kPHalf / 4);  // this warp's 4 KiB
+          uint8_t* prow = smem + pw + (lane >> 3) * 1024 + (lane & 7) * 64;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint8_t* at = prow + ((u ^ ((lane >> 1) & 3)) << 4);
+            *reinterpret_cast<uint4*>(at) = make_uint4(r[8 * u], r[8 * u + 1], r[8 * u + 2], r[8 * u + 3]);
+            *reinterpret_cast<uint4*>(at + 512) = make_uint4(r[8 * u + 4], r[8 * u + 5], r[8 * u + 6], r[8 * u + 7]);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) bulk_peer(peer_smem + pw, smem_u32(smem) + pw, kPBytes / 8, px_bar);
+          if (lane == 0) bulk_peer(peer_smem + pw, smem_u32(smem) + pw, kPHalf / 4, px_bar);
         }
         ok = !dead;
         // the row's sum over its four threads; reference and sum go with the last tile's P
@@ -862,9 +888,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         quad_sync(q);
         if (h4 == 0) {
           l += sPair[128 + R] + sPair[256 + R] + sPair[384 + R];
-          const uint32_t sl = last & (kSlots - 1), px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + sl);
-          st_async_f32(peer_smem + kOffML + 4 * (256 * sl + R), fin, px_bar);
-          st_async_f32(peer_smem + kOffML + 4 * (256 * sl + 128 + R), l, px_bar);
+          const uint32_t ps = last & 1, px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + ps);
+          st_async_f32(peer_smem + kOffML + 4 * (256 * ps + R), fin, px_bar);
+          st_async_f32(peer_smem + kOffML + 4 * (256 * ps + 128 + R), l, px_bar);
         }
         // the last product is complete: the stages may take the next item's Q, and Q's place too
         if (ok) ok = warp_wait(&bars[B_SEG], seg & 1);
@@ -877,25 +903,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         }
         const bool arms = h == 0 && q == 0 && lane == 0;
         for (uint32_t i = i0; ok && i < it.nt; i += 2) {
-          const uint32_t m = n + i, sl = m & (kSlots - 1);
-          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + sl], kPBytes + 512 + (i + 1 == it.nt ? 1024 : 0));
-          ok = warp_wait_cluster(&bars[B_PXFULL + sl], (m >> 2) & 1);
-          const float a = sA[128 * sl + R];
+          const uint32_t m = n + i;
+          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + set], kPBytes + 512 + (i + 1 == it.nt ? 1024 : 0));
+          ok = warp_wait_cluster(&bars[B_PXFULL + set], (m >> 1) & 1);
+          const float a = sA[128 * set + R];
           if (__any_sync(0xffffffffu, a != 1.0f)) {  // O(m - 1) is complete, O(m) waits for this warp
-            ok = ok && warp_wait(&bars[B_PFREE + ((m - 1) & (kSlots - 1))], ((m - 1) >> 2) & 1);
+            ok = ok && warp_wait(&bars[B_PFREE + 2 * (set ^ 1) + 1], ((m - 1) >> 1) & 1);
             tc_fence_after();
             rescale_o(lane_addr + 256 * h, a);
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_PREADY + sl]);
+          if (lane == 0) mbar_arrive(&bars[B_PREADY + set]);
         }
         if (ok) ok = warp_wait(&bars[B_SEG], seg & 1);
         // ------------------------------ out ------------------------------
-        const uint32_t sl = last & (kSlots - 1);
-        if (ok) ok = warp_wait_cluster(&bars[B_PXFULL + sl], (last >> 2) & 1);
+        const uint32_t ps = last & 1;
+        if (ok) ok = warp_wait_cluster(&bars[B_PXFULL + ps], (last >> 1) & 1);
         tc_fence_after();
-        const float ref = sML[256 * sl + R], l = sML[256 * sl + 128 + R];
+        const float ref = sML[256 * ps + R], l = sML[256 * ps + 128 + R];
         const bool whole = it.tile0 == 0 && it.nt == s.tiles;
         const bool live = R < live_rows;
         const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
@@ -943,7 +969,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         tc_fence_before();
         // every warp has read O, the reference and the sum: the next item may start, the slot is free
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
-        if (tid == 0) mbar_arrive_peer(peer_smem + kOffBar + 8 * (B_PFREE + sl));
+        if (tid < 2) mbar_arrive_peer(peer_smem + kOffBar + 8 * (B_PFREE + 2 * ps + tid));
       }
       if (!ok) give_up();
       n += it.nt;

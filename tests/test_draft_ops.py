@@ -928,3 +928,69 @@ def test_a_captured_step_replays_with_what_the_tensors_hold_then(fk, B, T, n):
         for a, b in zip(got, (q, out, lse, rows, packed, scales)):
             assert torch.equal(a, b)
     assert fk.workspace_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------------------
+# what the probabilities keep
+# ----------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("B, T, H, n", [(1, 2, 64, 2), (3, 2, 5, 6), (1, 2, 64, 700), (2, 4, 64, 3000)])
+def test_tree_rows_that_cancel(fk, B, T, H, n):
+    """Rows in pairs w, -w of nearly the same probability: out is the small difference of large terms, so what a
+    probability loses shows beside the output's bf16. Queries have one channel, whose logits (|z| < 0.02) are
+    exact but for fp32's rounding. A probability: its exponent in fp32, at most 16 in size, 2^-21; ex2 2^-22; its two
+    parts 2^-21; the row's sum the same again: together below 2^-18 of A = sum p |v|. The accumulator takes two steps for
+    every 16 rows, and as many joins as there are parts (at most one per two tiles), 2^-23 each. A probability in
+    fp16 alone would be off by up to 2^-12."""
+    cap = n + T
+    g = gen(100 + n)
+    packed = torch.randint(0, 256, (B, cap // 2, 1, 256), generator=g, device=DEV).to(torch.uint8).repeat(1, 1, 2, 1)
+    packed[:, :, 1] ^= 0x88                     # the other sign
+    packed = packed.reshape(B, cap, 256)
+    packed[:, :, :8] = torch.randint(0, 256, (B, cap, 8), generator=g, device=DEV).to(torch.uint8)  # channels 0 .. 15 apart
+    scales = torch.randint(0x30, 0x58, (B, cap // 2, 1, 32), generator=g, device=DEV).to(torch.uint8).repeat(1, 1, 2, 1).reshape(B, cap, 32)
+    scales[:, :, 0] = 0x38                      # channels 0 .. 15: values up to 6
+    q = torch.zeros(B, T, H, 512, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = (1 + torch.arange(H, device=DEV) / 64).bfloat16()
+    mask = torch.full((B, T), (1 << T) - 1, dtype=torch.int64, device=DEV)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    scale = 2.0 ** -10
+    out, lse = fk.tree_attn_decode(q, packed.contiguous(), scales.contiguous(), lens, mask, sm_scale=scale)
+    for b in range(B):
+        v = cache_values(packed[b], scales[b])
+        p = torch.softmax(q[b].double().cpu() @ v.T * scale, -1)
+        want, A = p @ v, p @ v.abs()
+        steps = 2 * ((cap + 15) // 16) + (cap + 127) // 128
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -18 + steps * 2.0 ** -23) * A
+        off = (out[b].double().cpu() - want).abs()
+        assert (off <= tol).all(), f"off by {(off / A).max():.2e} of the terms, {((off - tol) / A).max():.2e} too much"
+
+
+@gpu
+@pytest.mark.parametrize("heavy", [0.0, 0.02])
+def test_tree_keeps_the_attention_tolerance(fk, heavy):
+    """The library's bounds on its attention, before the rounding to bf16: 5e-3 in every value, lse within 1e-4, also
+    where one row in fifty is a hundred times louder (with queries a hundred times softer, so that several of those
+    rows share the sum); and sparse_attn_decode's own values, rounded."""
+    B, T, H, n, d = 2, 3, 64, 1500, 512
+    cap = n + T
+    x = P.kv_rows_dev(77, 0, B, cap, d, torch.device(DEV), heavy=heavy)
+    packed, scales = torch.empty(B, cap, d // 2, dtype=torch.uint8, device=DEV), torch.empty(B, cap, d // 16, dtype=torch.uint8, device=DEV)
+    fk.kv_quant_fp4(x.view(-1, d), packed.view(-1, d // 2), scales.view(-1, d // 16))
+    q = torch.stack([synth.attn_query(77, t, B, H, d, device=torch.device(DEV)) for t in range(T)], 1)
+    q = (q * (0.01 if heavy else 1.0)).contiguous()
+    mask = torch.full((B, T), 7, dtype=torch.int64, device=DEV)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    out, lse = fk.tree_attn_decode(q, packed, scales, lens, mask, sm_scale=1.0)
+    for b in range(B):
+        v = cache_values(packed[b], scales[b])
+        z = q[b].double().cpu() @ v.T
+        want = torch.softmax(z, -1) @ v
+        off = (out[b].double().cpu() - want).abs()
+        assert (off <= P.ATTN_MAX_ABS + 2.0 ** -8 * (want.abs() + P.ATTN_MAX_ABS)).all(), f"off by {off.max():.2e}"
+        assert (lse[b].double().cpu() - torch.logsumexp(z, -1)).abs().max() <= P.LSE_ABS
+    idx = torch.arange(cap, dtype=torch.int32, device=DEV).repeat(B, 1)
+    one, l1 = fk.sparse_attn_decode(q[:, 0].contiguous(), packed, scales, lens + T, idx, 1.0)
+    assert ((one - out[:, 0].float()).abs() <= 2 * P.ATTN_MAX_ABS + 2.0 ** -8 * one.abs() + 2.0 ** -8 * P.ATTN_MAX_ABS).all()
+    assert (l1 - lse[:, 0]).abs().max() <= 2 * P.LSE_ABS
