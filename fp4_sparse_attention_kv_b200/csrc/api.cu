@@ -188,7 +188,7 @@ TreeLayout tree_layout(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int 
   off += up(sizeof(uint32_t) * (B + 2));
   L.part_ml = off;
   const int64_t parts = fp4kv::tree_always_whole(cap, top_k) ? 0 : 2 * L.n_clusters;
-  off += up(sizeof(float) * parts * 128 * 2);
+  off += up(sizeof(float) * parts * 128 * 4);
   L.part_o = off;
   off += up(sizeof(float) * parts * 128 * 512);
   L.total = off;

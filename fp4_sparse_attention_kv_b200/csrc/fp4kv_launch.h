@@ -148,7 +148,7 @@ struct TreeAttnParams {
   int n_clusters, min_tiles;  // tree_clusters(), tree_min_tiles()
   bool whole;                 // tree_whole_items(): items are not shared between clusters
   uint32_t* first_tile;       // workspace [B + 2]: each sequence's first tile, the number of tiles, the clusters in use
-  float* part_ml;             // workspace [2 n_clusters][128][2]: reference and sum of unfinished items
+  float* part_ml;             // workspace [2 n_clusters][128][4]: reference, sum and factor of S of unfinished items
   float* part_o;              // workspace [2 n_clusters][128][512]
   uint32_t* status;
 };

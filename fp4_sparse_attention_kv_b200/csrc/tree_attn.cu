@@ -29,9 +29,11 @@
 //    the odd ones. Scores: reference and sum in registers (lane = query row, 32 columns a thread);
 //    the reference is handed from set to set. Values: P's arrival, O's rescaling, the output.
 // Numerics: q as fp16 times a power of two per row (exact down to 2^-28 of the row's maximum), v exact
-// in fp16, S and O in fp32. The reference m moves only when a logit passes it by 2^9 (log2 domain),
-// to 2^-1 of the maximum; p is made as p * 2^6, so the row's largest is at least 2^7 and at most 2^15, and goes as two
-// fp16: its upper 11 bits and the rest, rounded to 11 bits. Together they are off by at most 2^-21 of p, or by
+// in fp16, S and O in fp32. A row's logits are c S (log2 domain). The reference m, a value of S, moves only when a
+// logit passes it by 2^8, to the maximum; p = 2^(c (S - m) + 7). The difference comes first: c S and c m rounded
+// apart, a row's largest p could be anything once a logit has no bits left below 1 (from 2^24 on). c is cut off at
+// 2^90 there, where it multiplies the least difference of two S (2^-34) to 2^56: one row has it all either way. A row's
+// largest p is at least 2^7 and at most 2^15, and goes as two fp16: its upper 11 bits and the rest, rounded to 11 bits. Together they are off by at most 2^-21 of p, or by
 // 2^-24, 2^-31 of the largest. One fp16 alone, 2^-12, would show where rows cancel, and breaks the library's
 // bound on its attention (5e-3 in every value) where some rows are a hundred times louder. The sums are fp32.
 // Every wait is bounded; on timeout a status bit is set and the kernel winds down.
@@ -55,7 +57,8 @@ constexpr int kStages = 2;  // tiles of V
 constexpr int kSlots = 4;   // tiles of S
 constexpr int kPSlots = 2;  // tiles of P: tile m's in slot m & 1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMoveLog2 = 9.0f, kHeadroomLog2 = -1.0f, kPLog2 = 6.0f;  // (in the log2 domain)
+constexpr float kMoveLog2 = 8.0f, kPLog2 = 7.0f;  // a reference moves past 2^8; p = 2^7 at it
+constexpr float kMostC = 0x1p90f;  // (S stays below 2^37)
 
 constexpr uint32_t kVChunk = kTile * 128;         // [64 rows][64 channels]
 constexpr uint32_t kVBytes = 8 * kVChunk;         // 64 KiB
@@ -70,8 +73,8 @@ constexpr uint32_t kOffC = kOffBar + 448;         // scores: [128] power of two 
 constexpr uint32_t kOffPair = kOffC + 512;        // scores: [4][128] exchange between a row's four threads
 constexpr uint32_t kOffRef = kOffPair + 2048;     // scores: [2][128] reference after the last tile of either parity
 constexpr uint32_t kOffA = kOffRef + 1024;        // values: [2 slots][128] factors of O
-constexpr uint32_t kOffML = kOffA + 1024;         // values: [2 slots][2][128] reference and sum, with an item's last tile
-constexpr uint32_t kSmem = kOffML + 2048;
+constexpr uint32_t kOffML = kOffA + 1024;         // values: [2 slots][3][128] reference, sum and c, with an item's last tile
+constexpr uint32_t kSmem = kOffML + 3072;
 static_assert(kSmem <= 232448, "shared memory");
 
 // TMEM columns. Scores: Q [0, 256), S slots [256, 512). Values: O [0, 512).
@@ -350,6 +353,10 @@ FP4KV_DEV void dequant_chunk(uint32_t at, uint32_t j, const uint32_t (&c)[8], ui
                  ::"r"(at ^ (16u * k)), "r"(hmul2_f16(h[0], sc[k >> 1])), "r"(hmul2_f16(h[1], sc[k >> 1])),
                    "r"(hmul2_f16(h[2], sc[k >> 1])), "r"(hmul2_f16(h[3], sc[k >> 1])) : "memory");
   }
+}
+
+FP4KV_DEV float lse_of(float ref, float l, float c) {
+  return l == 0.0f ? -INFINITY : fmaf(ref, c, -kPLog2) * kLn2 + logf(l);
 }
 
 // this thread's TMEM lane, 256 of its O columns, times a
@@ -761,9 +768,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         tmem_st_wait();
         // q = fp16 * 2^(low - 112)
         const int up = low - 112;
-        const float c = fmaxf(fabsf(p.sm_scale) * kLog2e * __uint_as_float(uint32_t(127 + up / 2) << 23) *
-                                  __uint_as_float(uint32_t(127 + (up - up / 2)) << 23),
-                              2e-38f);  // (above zero: a masked -inf stays -inf)
+        const float c = fminf(fmaxf(fabsf(p.sm_scale) * __uint_as_float(uint32_t(127 + up / 2) << 23) *
+                                        __uint_as_float(uint32_t(127 + (up - up / 2)) << 23) * kLog2e,
+                                    2e-38f),       // (above zero: a masked -inf stays -inf)
+                              3.4028235e38f);      // (finite: times a reference of 0 it is 0)
+        const float cc = fminf(c, kMostC);
         // the same bytes are written by the dequantizing warps next and read by the tensor cores
         tc_fence_before();
         __syncwarp();
@@ -778,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         bool e_ok = entry_ok(i0);
         float ref = -INFINITY;  // the reference that l2 is relative to
         uint64_t l2 = 0;        // the row's sum over even and odd columns
-        const uint64_t c2 = pack2(c, c);
+        const uint64_t c2 = pack2(cc, cc);
         // a wait that ran out ends the loop of both warps of a row at the next vote
         bool dead = !ok;
         for (uint32_t i = i0; i < it.nt; i += 2) {
@@ -804,7 +813,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           float mx = __uint_as_float(r[0]);
 #pragma unroll
           for (int k = 1; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]));
-          mx *= c;
           // the reference after the tile before, from the other set
           float old = -INFINITY;
           if (i > 0) {
@@ -812,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             old = sRef[128 * (set ^ 1) + R];
           }
           float to = old, a = 1.0f;
-          const bool moves = pair_any(pair, mx > old + kMoveLog2 || dead);
+          const bool moves = pair_any(pair, (mx - old) * cc > kMoveLog2 || dead);
           if (moves) {  // a reference of these 32 rows moves
             if (pair_any(pair, dead)) {
               dead = true;
@@ -821,9 +829,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             sPair[128 * (2 * set + h) + R] = mx;
             pair_sync(pair);
             mx = fmaxf(mx, sPair[128 * (2 * set + (h ^ 1)) + R]);
-            if (mx > old + kMoveLog2) {
-              to = mx + kHeadroomLog2;
-              if (i > 0) a = ex2(old - to);  // (O starts with the first tile; no reference so far: 0)
+            if ((mx - old) * cc > kMoveLog2) {
+              to = mx;
+              if (i > 0) a = ex2((old - to) * cc);  // (O starts with the first tile; no reference so far: 0)
             }
           }
           if (h == 0) {
@@ -832,19 +840,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             if (lane == 0) mbar_arrive(&bars[B_REF + set]);
           }
           if (to != ref) {
-            const float f = ex2(ref - to);
+            const float f = ex2((ref - to) * cc);
             l2 = fma2(l2, pack2(f, f), 0);
             ref = to;
           }
-          const float m6 = ref == -INFINITY ? -INFINITY : kPLog2 - ref;
-          const uint64_t m62 = pack2(m6, m6), kMinus1 = pack2(-1.0f, -1.0f);
+          const float base = ref == -INFINITY ? 0.0f : -ref;
+          const uint64_t base2 = pack2(base, base), k2 = pack2(kPLog2, kPLog2), kMinus1 = pack2(-1.0f, -1.0f);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {  // eight columns: their high parts, then their low parts, in the scores' place
             uint32_t w[4], v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float z0, z1;
-              unpack2(fma2(pack2(__uint_as_float(r[8 * u + 2 * k]), __uint_as_float(r[8 * u + 2 * k + 1])), c2, m62), z0, z1);
+              unpack2(fma2(add2(pack2(__uint_as_float(r[8 * u + 2 * k]), __uint_as_float(r[8 * u + 2 * k + 1])), base2), c2, k2), z0, z1);
               const float e0 = ex2(z0), e1 = ex2(z1);
               l2 = add2(l2, pack2(e0, e1));
               // the high part's 11 bits by truncation, so that the rest is exact
@@ -883,14 +891,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         float l, l1;
         unpack2(l2, l, l1);
         l += l1;
-        if (l > 0.0f) l *= ex2(ref - fin);
+        if (l > 0.0f) l *= ex2((ref - fin) * cc);
         if (h4 != 0) sPair[128 * h4 + R] = l;
         quad_sync(q);
         if (h4 == 0) {
           l += sPair[128 + R] + sPair[256 + R] + sPair[384 + R];
           const uint32_t ps = last & 1, px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + ps);
-          st_async_f32(peer_smem + kOffML + 4 * (256 * ps + R), fin, px_bar);
-          st_async_f32(peer_smem + kOffML + 4 * (256 * ps + 128 + R), l, px_bar);
+          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + R), fin, px_bar);
+          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + 128 + R), l, px_bar);
+          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + 256 + R), c, px_bar);
         }
         // the last product is complete: the stages may take the next item's Q, and Q's place too
         if (ok) ok = warp_wait(&bars[B_SEG], seg & 1);
@@ -904,7 +913,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         const bool arms = h == 0 && q == 0 && lane == 0;
         for (uint32_t i = i0; ok && i < it.nt; i += 2) {
           const uint32_t m = n + i;
-          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + set], kPBytes + 512 + (i + 1 == it.nt ? 1024 : 0));
+          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + set], kPBytes + 512 + (i + 1 == it.nt ? 1536 : 0));
           ok = warp_wait_cluster(&bars[B_PXFULL + set], (m >> 1) & 1);
           const float a = sA[128 * set + R];
           if (__any_sync(0xffffffffu, a != 1.0f)) {  // O(m - 1) is complete, O(m) waits for this warp
@@ -921,15 +930,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         const uint32_t ps = last & 1;
         if (ok) ok = warp_wait_cluster(&bars[B_PXFULL + ps], (last >> 1) & 1);
         tc_fence_after();
-        const float ref = sML[256 * ps + R], l = sML[256 * ps + 128 + R];
+        const float ref = sML[384 * ps + R], l = sML[384 * ps + 128 + R], c = sML[384 * ps + 256 + R];
         const bool whole = it.tile0 == 0 && it.nt == s.tiles;
         const bool live = R < live_rows;
         const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (NaN stays NaN)
         const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int ch = 128 * h4 + 32 * c;
+        for (int u = 0; u < 4; ++u) {
+          const int ch = 128 * h4 + 32 * u;
           uint32_t r[32];
           tmem_ld32(lane_addr + ch, r);
           tmem_ld_wait();
@@ -939,10 +948,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
             for (int k = 0; k < 2; ++k) {
               uint32_t w[8];
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
+              for (int v = 0; v < 8; ++v)
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                    : "=r"(w[u])
-                    : "f"(__uint_as_float(r[16 * k + 2 * u + 1]) * inv), "f"(__uint_as_float(r[16 * k + 2 * u]) * inv));
+                    : "=r"(w[v])
+                    : "f"(__uint_as_float(r[16 * k + 2 * v + 1]) * inv), "f"(__uint_as_float(r[16 * k + 2 * v]) * inv));
               if (al32) {
                 asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * k), "r"(w[0]), "r"(w[1]),
                              "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
@@ -962,9 +971,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         }
         if (live && h4 == 0) {
           if (!whole)
-            __stcg(reinterpret_cast<float2*>(p.part_ml) + slot * kRows + R, make_float2(ref, l));
+            __stcg(reinterpret_cast<float4*>(p.part_ml) + slot * kRows + R, make_float4(ref, l, c, 0.0f));
           else if (p.lse)
-            p.lse[row0 + R] = l == 0.0f ? -INFINITY : (ref - kPLog2) * kLn2 + logf(l);
+            p.lse[row0 + R] = lse_of(ref, l, c);
         }
         tc_fence_before();
         // every warp has read O, the reference and the sum: the next item may start, the slot is free
@@ -985,7 +994,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   }
 }
 
-// Joins the parts of items that several clusters worked on: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+// Joins the parts of items that several clusters worked on: o = sum_i 2^(c (m_i - M)) O_i / sum_i 2^(c (m_i - M)) l_i.
 // A block takes 32 query rows and 128 channels: lanes along the rows as the parts lie, then through shared
 // memory to lanes along the channels.
 constexpr int kMergeCh = 128;
@@ -1005,20 +1014,22 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
   const int R = r0 % kRows + lane, n = static_cast<int>(c1 - c0 + 1);
   const bool live = r0 + lane < n_rows;
   auto slot = [&](int i) { return int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)); };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + R;
+  const float4* ml = reinterpret_cast<const float4*>(p.part_ml) + R;
   const float4* po = reinterpret_cast<const float4*>(p.part_o) + (ch0 / 4 + warp) * kRows + R;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, c = 1.0f;
   float4 o[4] = {};  // fours warp, warp + 8, ... of the block's channels
   if (live) {
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
-      const float2 v = __ldcg(ml + slot(i) * kRows);
+      const float4 v = __ldcg(ml + slot(i) * kRows);  // reference, sum, c (the same in every part)
       float4 f[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = __ldcg(po + slot(i) * (kD / 4) * kRows + 8 * k * kRows);
       const float to = v.y > 0.0f ? fmaxf(m, v.x) : m;
-      const float w0 = m == to ? 1.0f : ex2(m - to), w1 = v.y > 0.0f ? ex2(v.x - to) : 0.0f;
+      const float cc = fminf(v.z, kMostC);
+      const float w0 = m == to ? 1.0f : ex2((m - to) * cc), w1 = v.y > 0.0f ? ex2((v.x - to) * cc) : 0.0f;
       m = to;
+      c = v.z;
       l = fmaf(w1, v.y, l * w0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -1036,7 +1047,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
     t[0] = o[k].x * inv; t[1] = o[k].y * inv; t[2] = o[k].z * inv; t[3] = o[k].w * inv;
   }
   const int64_t row0 = int64_t(b) * p.T * p.H + r0;
-  if (p.lse && blockIdx.y == 0 && warp == 0 && live) p.lse[row0 + lane] = l == 0.0f ? -INFINITY : (m - kPLog2) * kLn2 + logf(l);
+  if (p.lse && blockIdx.y == 0 && warp == 0 && live) p.lse[row0 + lane] = lse_of(m, l, c);
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

@@ -994,3 +994,32 @@ def test_tree_keeps_the_attention_tolerance(fk, heavy):
     one, l1 = fk.sparse_attn_decode(q[:, 0].contiguous(), packed, scales, lens + T, idx, 1.0)
     assert ((one - out[:, 0].float()).abs() <= 2 * P.ATTN_MAX_ABS + 2.0 ** -8 * one.abs() + 2.0 ** -8 * P.ATTN_MAX_ABS).all()
     assert (l1 - lse[:, 0]).abs().max() <= 2 * P.LSE_ABS
+
+
+@gpu
+@pytest.mark.parametrize("n", [100, 3000])  # (whole items, and items in parts)
+@pytest.mark.parametrize("loud, scale", [(1.0, 1e3), (1e3, 1e4), (1e6, 1e6), (1e20, 1e-3), (1e37, 1e3), (1e-30, 3e38), (1e3, -1e7)])
+def test_tree_logits_beyond_what_fp32_counts(fk, n, loud, scale):
+    """Logits from 1e5 to past fp32's range: every head gives the one row that wins, which is exact in bf16 (6 bits);
+    lse is the winner's logit. Heads whose second row is within what a logit may be off by, and 40, are left out: the
+    other rows' weights are together below 3003 e^-40 < 2^-46, their values below 2^12, so out is off by at most 2^-33
+    (less than bf16's step at any value of the cache but 0)."""
+    B, T, H = 1, 3, 64
+    packed, scales = make_cache(fk, B, n + T, 120)
+    q = (torch.randn(B, T, H, 512, generator=gen(121), device=DEV) * loud).bfloat16()
+    mask = torch.full((B, T), 7, dtype=torch.int64, device=DEV)
+    out, lse = fk.tree_attn_decode(q, packed, scales, torch.tensor([n], dtype=torch.int32, device=DEV), mask, sm_scale=scale)
+    v = cache_values(packed[0], scales[0])
+    qq = q[0].double().cpu()
+    scale32 = float(np.float32(scale))
+    z = qq @ v.T * scale32
+    dz = 2.0 ** -16 * abs(scale32) * (qq.abs() @ v.abs().T).amax(-1)
+    top = z.topk(2, -1)
+    sure = top.values[..., 0] - top.values[..., 1] > 2 * dz + 40.0
+    assert sure.double().mean() > 0.9
+    assert torch.isfinite(out).all()
+    assert ((out[0].double().cpu() - v[top.indices[..., 0]]).abs()[sure] <= 2.0 ** -33).all()
+    l, want = lse[0].double().cpu()[sure], top.values[..., 0][sure]
+    far = want.abs() > 3.4e38  # (past the type)
+    assert torch.equal(l[far], torch.sign(want[far]) * np.inf)
+    assert ((l - want).abs() <= dz[sure] + 2.0 ** -21 * want.abs())[~far].all()
