@@ -149,7 +149,7 @@ struct TreeAttnParams {
   bool whole;                 // tree_whole_items(): items are not shared between clusters
   uint32_t* first_tile;       // workspace [B + 2]: each sequence's first tile, the number of tiles, the clusters in use
   float* part_ml;             // workspace [2 n_clusters][128][4]: reference, sum and factor of S of unfinished items
-  float* part_o;              // workspace [2 n_clusters][128][512]
+  float* part_o;              // workspace [2 n_clusters][128][512]: their O; and an item's O as far as it has been added up
   uint32_t* status;
 };
 // Tiles at most (below 2^32), clusters of two CTAs for sequences of `rows` = T * H query rows, and the

@@ -56,6 +56,12 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole warpgroups: registers m
 constexpr int kStages = 2;  // tiles of V
 constexpr int kSlots = 4;   // tiles of S
 constexpr int kPSlots = 2;  // tiles of P: tile m's in slot m & 1
+// Tiles that are added up in TMEM at most. The tensor core's fp32 sums are cut off, not rounded: each of the 8
+// steps of a tile loses half an ulp of O on average, always towards zero (2^-14 after 256 tiles; 2^-8 after 16,384). After
+// kFlush tiles of an item O goes to the workspace, where it is added with rounding, and starts again from zero; a row's
+// sum is kept in as many parts. Costs 3 % from 512 tiles on (661 against 643 us for 8,192 query rows over 32,832);
+// without it a prefix of 1,000,000 rows came out 0.4 to 0.8 % too small.
+constexpr uint32_t kFlush = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMoveLog2 = 8.0f, kPLog2 = 7.0f;  // a reference moves past 2^8; p = 2^7 at it
 constexpr float kMostC = 0x1p90f;  // (S stays below 2^37)
@@ -72,9 +78,11 @@ constexpr uint32_t kOffIter = kOffBar + 336;      // the cluster's range (a SegI
 constexpr uint32_t kOffC = kOffBar + 448;         // scores: [128] power of two of the query rows
 constexpr uint32_t kOffPair = kOffC + 512;        // scores: [4][128] exchange between a row's four threads
 constexpr uint32_t kOffRef = kOffPair + 2048;     // scores: [2][128] reference after the last tile of either parity
-constexpr uint32_t kOffA = kOffRef + 1024;        // values: [2 slots][128] factors of O
-constexpr uint32_t kOffML = kOffA + 1024;         // values: [2 slots][3][128] reference, sum and c, with an item's last tile
-constexpr uint32_t kSmem = kOffML + 3072;
+constexpr uint32_t kOffFlushed = kOffRef + 1024;  // scores: [128] reference of what has been flushed
+constexpr uint32_t kOffSum = kOffFlushed + 512;   // scores: [512] a thread's share of its row's sum, without the last tiles'
+constexpr uint32_t kOffA = kOffSum + 2048;        // values: [2 slots][128] factors of O
+constexpr uint32_t kOffML = kOffA + 1024;         // values: [2 slots][4][128] with an item's last tile: reference, sum, c, factor of what lies aside
+constexpr uint32_t kSmem = kOffML + 4096;
 static_assert(kSmem <= 232448, "shared memory");
 
 // TMEM columns. Scores: Q [0, 256), S slots [256, 512). Values: O [0, 512).
@@ -355,6 +363,40 @@ FP4KV_DEV void dequant_chunk(uint32_t at, uint32_t j, const uint32_t (&c)[8], ui
   }
 }
 
+// kCols of this thread's O (its TMEM lane) plus a times what the workspace has of them (first: nothing yet): to there,
+// or with kBack to TMEM. 16 columns at a time: with 32 the loop's registers cost the kernel 200 bytes of spills.
+template <int kCols, bool kBack>
+FP4KV_DEV void flush_o(uint32_t addr, float4* w, float a, bool first, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < kCols / 16; ++c) {
+    uint32_t r[16];
+    tmem_ld16(addr + 16 * c, r);
+    tmem_ld_wait();
+    if (live) {
+      if (!first) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = __ldcg(w + k * kRows);
+          r[4 * k] = __float_as_uint(fmaf(v.x, a, __uint_as_float(r[4 * k])));
+          r[4 * k + 1] = __float_as_uint(fmaf(v.y, a, __uint_as_float(r[4 * k + 1])));
+          r[4 * k + 2] = __float_as_uint(fmaf(v.z, a, __uint_as_float(r[4 * k + 2])));
+          r[4 * k + 3] = __float_as_uint(fmaf(v.w, a, __uint_as_float(r[4 * k + 3])));
+        }
+      }
+      if (!kBack) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          __stcg(w + k * kRows, make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                            __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])));
+      }
+    }
+    w += 4 * kRows;
+    __syncwarp();
+    if (kBack) tmem_st16(addr + 16 * c, r);
+  }
+  if (kBack) tmem_st_wait();
+}
+
 FP4KV_DEV float lse_of(float ref, float l, float c) {
   return l == 0.0f ? -INFINITY : fmaf(ref, c, -kPLog2) * kLn2 + logf(l);
 }
@@ -379,6 +421,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   int* sLow = reinterpret_cast<int*>(smem + kOffC);
   float* sPair = reinterpret_cast<float*>(smem + kOffPair);
   float* sRef = reinterpret_cast<float*>(smem + kOffRef);
+  float* sFlushed = reinterpret_cast<float*>(smem + kOffFlushed);
+  float* sSum = reinterpret_cast<float*>(smem + kOffSum);
   const float* sA = reinterpret_cast<const float*>(smem + kOffA);
   const float* sML = reinterpret_cast<const float*>(smem + kOffML);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -671,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
                       umma_ss<kHigh64, kHigh128>(go, tm + 256 * c, a0 + 2 * k + 32 * part, b0 + ((2048 * k + 4 * c * kVChunk) >> 4), kIdesc,
-                                                 i > 0 || (hf | k | part) != 0);
+                                                 (i & (kFlush - 1)) != 0 || (hf | k | part) != 0);
                 commit_if(go, &bars[B_VFREE + 2 * st + hf]);
                 // (an item's last slot is given back after its reference and sum have been read)
                 commit_to_if(go, &bars[B_PFREE + 2 * ps + hf], i + 1 < it.nt ? 3 : 2);
@@ -786,7 +830,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         };
         bool e_ok = entry_ok(i0);
         float ref = -INFINITY;  // the reference that l2 is relative to
-        uint64_t l2 = 0;        // the row's sum over even and odd columns
+        uint64_t l2 = 0;        // the row's sum over even and odd columns, of at most kFlush tiles
+        sSum[tid] = 0.0f;       // and over the tiles before
+        if (i0 == 0 && h == 0) sFlushed[R] = -INFINITY;  // the reference of what the workspace has of O
         const uint64_t c2 = pack2(cc, cc);
         // a wait that ran out ends the loop of both warps of a row at the next vote
         bool dead = !ok;
@@ -842,7 +888,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           if (to != ref) {
             const float f = ex2((ref - to) * cc);
             l2 = fma2(l2, pack2(f, f), 0);
+            sSum[tid] *= f;
             ref = to;
+          }
+          if (i > 1 && (i & (kFlush - 2)) == 0) {  // (either set's first tile of the next kFlush)
+            float l0, l1;
+            unpack2(l2, l0, l1);
+            sSum[tid] += l0 + l1;
+            l2 = 0;
+            if ((i & 1) == 0 && h == 0) {  // O goes to the workspace: the factor is that of what lies there
+              a = sFlushed[R] == -INFINITY ? 0.0f : ex2((sFlushed[R] - old) * cc);
+              sFlushed[R] = old;
+            }
           }
           const float base = ref == -INFINITY ? 0.0f : -ref;
           const uint64_t base2 = pack2(base, base), k2 = pack2(kPLog2, kPLog2), kMinus1 = pack2(-1.0f, -1.0f);
@@ -888,19 +945,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         // the row's sum over its four threads; reference and sum go with the last tile's P
         quad_sync(q);
         const float fin = sRef[128 * (last & 1) + R];
-        float l, l1;
-        unpack2(l2, l, l1);
-        l += l1;
+        float l0, l1;
+        unpack2(l2, l0, l1);
+        float l = sSum[tid] + (l0 + l1);
         if (l > 0.0f) l *= ex2((ref - fin) * cc);
         if (h4 != 0) sPair[128 * h4 + R] = l;
         quad_sync(q);
+        const uint32_t ml = peer_smem + kOffML + 4 * (512 * (last & 1) + R), ml_bar = peer_smem + kOffBar + 8 * (B_PXFULL + (last & 1));
         if (h4 == 0) {
           l += sPair[128 + R] + sPair[256 + R] + sPair[384 + R];
-          const uint32_t ps = last & 1, px_bar = peer_smem + kOffBar + 8 * (B_PXFULL + ps);
-          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + R), fin, px_bar);
-          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + 128 + R), l, px_bar);
-          st_async_f32(peer_smem + kOffML + 4 * (384 * ps + 256 + R), c, px_bar);
+          st_async_f32(ml, fin, ml_bar);
+          st_async_f32(ml + 512, l, ml_bar);
+          st_async_f32(ml + 1024, c, ml_bar);
         }
+        if (i0 == 0 && h == 0)  // the set that flushes
+          st_async_f32(ml + 1536, sFlushed[R] == -INFINITY ? 0.0f : ex2((sFlushed[R] - fin) * cc), ml_bar);
         // the last product is complete: the stages may take the next item's Q, and Q's place too
         if (ok) ok = warp_wait(&bars[B_SEG], seg & 1);
         quad_sync(q);  // (the sums have been read)
@@ -911,15 +970,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
           lane_addr = tmem + (uint32_t(32 * q) << 16);
         }
         const bool arms = h == 0 && q == 0 && lane == 0;
+        // this thread's row in the workspace (a whole item's slot is free: the one that another would begin in)
+        auto part = [&]() { return reinterpret_cast<float4*>(p.part_o) + int64_t(2 * cl + (it.tile0 == 0 ? 1 : 0)) * (kD / 4) * kRows + R; };
         for (uint32_t i = i0; ok && i < it.nt; i += 2) {
           const uint32_t m = n + i;
-          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + set], kPBytes + 512 + (i + 1 == it.nt ? 1536 : 0));
+          if (arms) mbar_arrive_expect_tx(&bars[B_PXFULL + set], kPBytes + 512 + (i + 1 == it.nt ? 2048 : 0));
           ok = warp_wait_cluster(&bars[B_PXFULL + set], (m >> 1) & 1);
           const float a = sA[128 * set + R];
-          if (__any_sync(0xffffffffu, a != 1.0f)) {  // O(m - 1) is complete, O(m) waits for this warp
+          const bool flush = i > 0 && (i & (kFlush - 1)) == 0;
+          if (flush || __any_sync(0xffffffffu, a != 1.0f)) {  // O(m - 1) is complete, O(m) waits for this warp
             ok = ok && warp_wait(&bars[B_PFREE + 2 * (set ^ 1) + 1], ((m - 1) >> 1) & 1);
             tc_fence_after();
-            rescale_o(lane_addr + 256 * h, a);
+            if (flush)
+              flush_o<256, false>(lane_addr + 256 * h, part() + 64 * h * kRows, a, i == kFlush, R < live_rows);
+            else
+              rescale_o(lane_addr + 256 * h, a);
           }
           tc_fence_before();
           __syncwarp();
@@ -930,8 +995,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
         const uint32_t ps = last & 1;
         if (ok) ok = warp_wait_cluster(&bars[B_PXFULL + ps], (last >> 1) & 1);
         tc_fence_after();
-        const float ref = sML[384 * ps + R], l = sML[384 * ps + 128 + R], c = sML[384 * ps + 256 + R];
+        const float ref = sML[512 * ps + R], l = sML[512 * ps + 128 + R], c = sML[512 * ps + 256 + R];
         const bool whole = it.tile0 == 0 && it.nt == s.tiles;
+        if (it.nt > kFlush) {
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");  // (what others have flushed)
+          flush_o<128, true>(lane_addr + 128 * h4, part() + 32 * h4 * kRows, sML[512 * ps + 384 + R], false, R < live_rows);
+        }
         const bool live = R < live_rows;
         const int slot = 2 * cl + (it.tile0 == 0 ? 1 : 0);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (NaN stays NaN)
@@ -1073,6 +1142,7 @@ int tree_min_tiles() { return 2; }
 // 25.0; 16 items of 5 19.8 against 23.8; 96 items of 9 42.0 against 51.0, of 15 55.8 against 61.1, of 22 72.6
 // against 71.1; 128 items of 8 40.5 against 58.4.
 constexpr int64_t kSegment = 8, kSharing = 17, kMostWhole = 20;
+static_assert(kMostWhole < int64_t(kFlush) && kFlush % 2 == 0, "whole items have no workspace; one set flushes");
 static int64_t tree_item_tiles(int64_t cap, int64_t top_k) { return ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile; }
 
 bool tree_always_whole(int64_t cap, int64_t top_k) { return tree_item_tiles(cap, top_k) + kSegment <= kSharing; }

@@ -1023,3 +1023,62 @@ def test_tree_logits_beyond_what_fp32_counts(fk, n, loud, scale):
     far = want.abs() > 3.4e38  # (past the type)
     assert torch.equal(l[far], torch.sign(want[far]) * np.inf)
     assert ((l - want).abs() <= dz[sure] + 2.0 ** -21 * want.abs())[~far].all()
+
+
+@gpu
+@pytest.mark.parametrize("spread", [True, False])
+@pytest.mark.parametrize("B, T, H, n", [(1, 64, 128, 1_000_000), (80, 1, 5, 120_000), (1, 64, 128, 16_800), (3, 64, 64, 16_400)])
+def test_tree_long_prefixes_do_not_drift(fk, B, T, H, n, spread):
+    """Every row has 1.0 in its last 496 channels, so out is 1.0 there, whatever the probabilities are (n of them, of many
+    sizes or all but one of the same): what a long sum of them loses is lost by the values or by the row's sum alone,
+    and shows as soon as it passes 2^-9. O is summed over at most 256 tiles (2,048 steps, each off by up to 2^-23: 2^-12)
+    and then with rounding, the sum of a row over 2,048 terms a thread (half of 2^-23 each) and then likewise."""
+    cap = n + T
+    g = gen(130)
+    packed = torch.full((B, cap, 256), 0x22, dtype=torch.uint8, device=DEV)
+    packed[:, :, :8] = torch.randint(0, 256, (B, cap, 8), generator=g, device=DEV).to(torch.uint8) if spread else 0x11
+    if not spread:
+        packed[:, 5, :8] = 0x77  # one row's logit is larger
+    scales = torch.full((B, cap, 32), 0x38, dtype=torch.uint8, device=DEV)
+    q = torch.zeros(B, T, H, 512, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = (1 + torch.arange(H, device=DEV) / 128).bfloat16()
+    mask = torch.ones(B, T, dtype=torch.int64, device=DEV)
+    out, lse = fk.tree_attn_decode(q, packed, scales, torch.full((B,), n, dtype=torch.int32, device=DEV), mask, sm_scale=0.37)
+    assert (out[..., 16:] == 1.0).all(), f"{out[..., 16:].min().item()} .. {out[..., 16:].max().item()}"
+    for b in range(0, B, 40):
+        v0 = cache_values(packed[b, :, :8].repeat(1, 32), scales[b])[: n + 1, 0]
+        for h in (0, H - 1):
+            z = v0 * q[b, 0, h, 0].double().cpu() * float(np.float32(0.37))
+            p = torch.softmax(z, -1)
+            assert abs(lse[b, 0, h].item() - torch.logsumexp(z, -1).item()) <= 2.0 ** -11
+            assert abs(out[b, 0, h, 0].item() - (p @ v0).item()) <= 2.0 ** -8 * abs((p @ v0).item()) + 2.0 ** -10 * (p @ v0.abs()).item()
+
+
+@gpu
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("B, T, H, n", [(1, 64, 128, 40_000), (2, 33, 128, 33_000), (1, 37, 128, 80_000)])  # (whole items, and parts)
+def test_tree_references_that_move_between_flushes(fk, B, T, H, n, rising):
+    """Logits that grow (or shrink) by 2^13 in all along a prefix of several times 256 tiles: what has been put
+    aside is scaled down again and again, or stays. The bound of test_tree_rows_that_cancel, with 2,048 steps."""
+    cap = n + T
+    g = gen(140)
+    packed = torch.randint(0, 256, (B, cap, 256), generator=g, device=DEV).to(torch.uint8)
+    scales = torch.randint(0x30, 0x40, (B, cap, 32), generator=g, device=DEV).to(torch.uint8)
+    ramp = torch.linspace(0x08, 0x60, cap, device=DEV)
+    scales[:, :, 0] = (ramp if rising else ramp.flip(0)).to(torch.uint8)
+    packed[:, :, 0] = 0x77
+    q = torch.zeros(B, T, H, 512, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = (1 + torch.arange(H, device=DEV) / 128).bfloat16()
+    mask = tree_masks(B, T, 8)
+    out, lse = fk.tree_attn_decode(q, packed, scales, torch.full((B,), n, dtype=torch.int32, device=DEV), mask, sm_scale=0.11)
+    for b in range(B):
+        v = cache_values(packed[b], scales[b]).to(DEV)
+        for t in (0, T - 1):
+            z = v[:, 0] * float(np.float32(0.11)) * q[b, t, :, :1].double()
+            m = int(mask[b, t])
+            z[:, n:][:, [not m >> j & 1 for j in range(T)]] = -np.inf
+            p = torch.softmax(z, -1)
+            want, A = p @ v, p @ v.abs()
+            off = (out[b, t].double() - want).abs()
+            assert (off <= 2.0 ** -8 * want.abs() + (2.0 ** -17 + 2.0 ** -12) * A).all(), f"{(off / A).max():.2e}"
+            assert ((lse[b, t].double() - torch.logsumexp(z, -1)).abs() <= 2.0 ** -11 + 2.0 ** -21 * torch.logsumexp(z, -1).abs()).all()
