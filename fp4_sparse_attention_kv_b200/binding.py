@@ -502,9 +502,12 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
     """Attention of T drafted tokens per sequence, a tree, over the FP4 cache: q bf16 [B, T, H,
     512]; packed uint8 [B, cap, 256]; scales uint8 [B, cap, 32]; prefix_lens int32 [B];
     tree_mask int64 [B, T] (bit j: the token sees draft j, whose row is prefix_lens + j);
-    n_draft (optional) int32 [B]; idx (optional) int32 [B, top_k]: the prefix positions to
-    attend (every one without it). Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
+    n_draft (optional) int32 [B]; idx (optional) int32 [B, top_k], top_k >= 1: the prefix positions to
+    attend (every one without it; rows of -1: none). Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
     None); tokens behind n_draft keep what their outputs held."""
+    if idx is not None and (idx.dim() != 2 or idx.shape[1] < 1):
+        # (the address of no entries is null, which the library takes for no selection)
+        raise ValueError("idx: expected [B, top_k] with top_k >= 1 (a selection of nothing: one column of -1)")
     dev = q.get_device()
     if dev < 0:
         raise TypeError("q: expected a CUDA tensor")
@@ -527,7 +530,7 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
     top_k = 0
     if idx is not None:
         idx_at = _take(idx, _INT32, "idx", dev)
-        if idx.dim() != 2 or idx.shape[0] != B:
+        if idx.shape[0] != B:
             raise ValueError("idx: expected [B, top_k]")
         top_k = idx.shape[1]
     if out is None:

@@ -221,6 +221,28 @@ def test_a_tree_workspace_for_a_batch_serves_every_smaller_one(cap, top_k):
         assert sizes[at:at + 159] == sorted(sizes[at:at + 159])
 
 
+@pytest.mark.parametrize("shape", [(2, 0), (0, 0), (2,), (2, 1, 4)])
+def test_binding_refuses_a_selection_without_entries(shape):
+    """Its address is null, the library's word for "every row"."""
+    idx = torch.empty(shape, dtype=torch.int32)
+    assert idx.numel() or idx.data_ptr() == 0
+    with pytest.raises(ValueError, match="idx"):
+        binding.tree_attn_decode(torch.zeros(2, 1, 1, 512, dtype=torch.bfloat16), None, None, None, None, idx=idx)
+
+
+@gpu
+def test_tree_a_selection_of_nothing(fk):
+    """Refused without a column, the drafts alone with one column of -1."""
+    B, T, H, n = 2, 3, 10, 200
+    packed, scales = make_cache(fk, B, n + T, 150)
+    q = torch.randn(B, T, H, 512, generator=gen(151), device=DEV).bfloat16()
+    lens, mask = torch.tensor([n, 77], dtype=torch.int32, device=DEV), tree_masks(B, T, 2)
+    with pytest.raises(ValueError, match="idx"):
+        fk.tree_attn_decode(q, packed, scales, lens, mask, idx=torch.empty(B, 0, dtype=torch.int32, device=DEV))
+    run_tree(fk, B, T, H, [n, 77], None, n + T, idx=torch.full((B, 1), -1, dtype=torch.int32, device=DEV), q=q, mask=mask,
+             cache=(packed, scales))
+
+
 def test_binding_refuses_cpu_tensors_and_missing_arguments():
     x = torch.zeros(2, 512, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
