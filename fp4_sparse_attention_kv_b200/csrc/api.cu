@@ -3,6 +3,7 @@
 // include/fp4kv.h. Nothing here allocates device memory or synchronises (except
 // fp4kv_workspace_status, a diagnostic call documented as synchronising).
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -713,6 +714,7 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
   if (!aligned(q, 16) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(out, 16) || !aligned(tree_mask, 8) ||
       !aligned(idx, 4) || !aligned(ws, kAlign))
     return fail(FP4KV_ERR_INVALID_ARG, "misaligned q/packed/scales/out (16 B), tree_mask (8 B) or ws (256 B)");
+  if (!std::isfinite(sm_scale)) return fail(FP4KV_ERR_INVALID_ARG, "sm_scale=%g must be finite", sm_scale);
   const int sms = num_sms();
   if (fp4kv::tree_tiles(B, int64_t(T) * H, cap, top_k) >= (int64_t(1) << 32))
     return fail(FP4KV_ERR_UNSUPPORTED, "B=%d sequences of %lld query rows over cap=%lld rows: 2^32 tiles or more", B,

@@ -312,6 +312,8 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  * nothing gets out = 0, lse = -inf. A row that no token sees is not read. A cache row with a NaN
  * scale gives NaN to the tokens that see it and to no others; a query head with an infinity or
  * NaN gives NaN (unless its token sees nothing).
+ * sm_scale is finite, of any size and sign: logits beyond what fp32 counts give the row that wins, an lse
+ * beyond its range is infinite.
  * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without;
  * B * ceil(T H / 128) * ceil((R + 64) / 64) < 2^32 with R = top_k or cap. ws: at least
  * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,

@@ -230,6 +230,14 @@ def test_binding_refuses_a_selection_without_entries(shape):
         binding.tree_attn_decode(torch.zeros(2, 1, 1, 512, dtype=torch.bfloat16), None, None, None, None, idx=idx)
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf"), 1e39])
+def test_tree_refuses_a_scale_that_is_not_finite(scale):
+    """A NaN scale gave every token the mean of what it sees."""
+    args = [FAKE, 2, 5, 64, 512, FAKE, FAKE, 100, FAKE, None, FAKE, None, 0, ctypes.c_float(scale), FAKE, None, FAKE, 1 << 30, None]
+    st, msg = _c("fp4kv_tree_attn_decode", *args)
+    assert st == 1 and "sm_scale" in msg, (st, msg)
+
+
 @gpu
 def test_tree_a_selection_of_nothing(fk):
     """Refused without a column, the drafts alone with one column of -1."""
