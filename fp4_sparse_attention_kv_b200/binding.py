@@ -170,7 +170,8 @@ def workspace_init(ws: torch.Tensor):
 
 
 def alloc_workspace(nbytes: int, device) -> torch.Tensor:
-    """Allocate (with torch) and zero a workspace of at least nbytes (256-byte aligned)."""
+    """Allocate (with torch) and zero a workspace of at least nbytes (256-byte aligned), for one op:
+    workspace_init it again before an indexer op uses what another op, or other sizes, have used."""
     ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     workspace_init(ws)
     return ws

@@ -101,9 +101,15 @@ const char* fp4kv_version(void);
 size_t fp4kv_workspace_bytes(int32_t op, int32_t B, int64_t cap, int32_t heads, int32_t top_k,
                              int32_t n_pool_blocks);
 
-/* Zero a workspace before its first use (enqueued on `stream`). Kernels leave the
- * workspace zeroed again when they finish, so it can be reused by later calls on the same
- * stream and captured in CUDA graphs; calls that share one workspace must not overlap. */
+/* Zero a workspace before its first use (enqueued on `stream`). A workspace then serves one
+ * op: any number of later calls of it on the same stream, captured in CUDA graphs too; calls
+ * that share one workspace must not overlap. The indexer ops (INDEXER_TOPK, REINDEX_TOPK,
+ * HIER_POOL_SELECT) count into a histogram that has to be zero when they start. They leave it
+ * zero, and scores around it, at places that depend on B, cap, top_k and n_pool_blocks; the
+ * attention ops (SPARSE_ATTN, TREE_ATTN) leave partial sums everywhere. So before an indexer op
+ * uses a workspace that another op, or an indexer op of other sizes, has used, zero it again
+ * with this call: without it the op may select wrong positions. SPARSE_ATTN and TREE_ATTN read
+ * nothing that they have not written, and may follow any op, of any sizes, without it. */
 fp4kv_status fp4kv_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Device status word of a workspace: bit 0 set if a kernel gave up on a bounded wait.
@@ -317,7 +323,7 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without;
  * B * ceil(T H / 128) * ceil((R + 64) / 64) < 2^32 with R = top_k or cap. ws: at least
  * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,
- * initialised once. q, packed, scales and out 16-byte aligned. */
+ * initialised once (fp4kv_workspace_init says what an indexer op needs behind it). q, packed, scales and out 16-byte aligned. */
 fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int32_t H, int32_t d,
                                     const uint8_t* packed, const uint8_t* scales, int64_t cap,
                                     const int32_t* prefix_lens, const int32_t* n_draft, const uint64_t* tree_mask,

@@ -1112,3 +1112,39 @@ def test_tree_references_that_move_between_flushes(fk, B, T, H, n, rising):
             off = (out[b, t].double() - want).abs()
             assert (off <= 2.0 ** -8 * want.abs() + (2.0 ** -17 + 2.0 ** -12) * A).all(), f"{(off / A).max():.2e}"
             assert ((lse[b, t].double() - torch.logsumexp(z, -1)).abs() <= 2.0 ** -11 + 2.0 ** -21 * torch.logsumexp(z, -1).abs()).all()
+
+
+@gpu
+def test_one_workspace_for_several_ops(fk):
+    """Attention and tree calls may follow any op on a workspace; an indexer call follows another op, or other sizes,
+    after workspace_init."""
+    B, T, H, cap, K, dev = 2, 4, 64, 6000, 512, torch.device(DEV)
+    lens = torch.tensor([cap - T, 4321], dtype=torch.int32, device=dev)
+    packed, scales = make_cache(fk, B, cap, 160)
+    mask = tree_masks(B, T, 9)
+    q = torch.randn(B, T, H, 512, generator=gen(161), device=dev).bfloat16()
+    qi, w = synth.indexer_query(5, 0, B, 32, device=dev)
+    keys = P.keys_dev(5, B, cap, True, dev)
+    need = [fk.workspace_bytes(fk.OP_TREE_ATTN, B, cap, T * H, top_k) for top_k in (0, K)]
+    need += [fk.workspace_bytes(fk.OP_INDEXER_TOPK, B, cap, 32, K), fk.workspace_bytes(fk.OP_SPARSE_ATTN, B, cap, H, K)]
+    ws = fk.alloc_workspace(max(need), dev)
+
+    def select(ws=None, n=cap):
+        return fk.indexer_topk(qi, w, keys[:, :n].contiguous(), lens.clamp(max=n), K, ws=ws)
+
+    def tree(idx, ws=None):
+        return fk.tree_attn_decode(q, packed, scales, lens, mask, idx=idx, sm_scale=0.04, ws=ws)
+
+    def sparse(idx, ws=None):
+        return fk.sparse_attn_decode(q[:, 0].contiguous(), packed, scales, lens, idx, 0.04, ws=ws)
+
+    idx, small = select(), select(n=3000)
+    dense, chosen, one = tree(None), tree(idx), sparse(idx)
+    for _ in range(2):
+        for n, want in ((cap, idx), (3000, small)):
+            fk.workspace_init(ws)
+            for _ in range(2):
+                assert torch.equal(select(ws, n), want)
+            for got, ref in ((tree(None, ws), dense), (tree(idx, ws), chosen), (sparse(idx, ws), one), (tree(None, ws), dense)):
+                assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert fk.workspace_status(ws) == 0
