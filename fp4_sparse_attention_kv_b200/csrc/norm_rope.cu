@@ -212,11 +212,13 @@ FP4KV_DEV void query_heads(const NormRopeParams& p, uint32_t ring, int64_t tok, 
 #pragma unroll
     for (int g = 0; g < GPL; ++g) {
       if (!there[g] || h >= h1) continue;
+      // (outside the rotated channels Q is 0, but 0 times an infinite neighbour would be NaN: two zeros instead)
+      const uint32_t swap = rot[g] ? 0x1032u : 0x4444u;
       uint32_t y[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         uint64_t t = mul2(widen2(x[g][k]), P[g][k]);
-        if (kPairs == kNeighbours) t = fma2(widen2(__byte_perm(x[g][k], 0, 0x1032)), Q[g][k], t);
+        if (kPairs == kNeighbours) t = fma2(widen2(__byte_perm(x[g][k], 0, swap)), Q[g][k], t);
         if (kPairs == kHalves) t = fma2(widen2(xp[g][k]), Q[g][k], t);
         float y0, y1;
         unpack2(mul2(t, r2), y0, y1);

@@ -267,7 +267,8 @@ fp4kv_status fp4kv_swa_quant_fp8(const uint16_t* x, int64_t n_rows, int32_t d, i
  *   the last rope_dim in pairs (a, b) with the token's (c, s): y_a = (u_a c - u_b s) * r,
  *   y_b = (u_b c + u_a s) * r. The pairs are neighbours (2j, 2j + 1), or with rope_half != 0
  *   (j, j + rope_dim / 2), counted from channel d - rope_dim.
- * Queries are computed in fp32 and rounded once to bf16. The KV row is the nearest fp32 value
+ * Queries are computed in fp32 and rounded once to bf16 (a head whose sum of squares passes
+ * fp32's range, with channels of 1e19, has r = 0 and gives zeros). The KV row is the nearest fp32 value
  * of y (held in 64 bits) rounded to bf16 (kv_out, nullable), and that bf16 row is quantized
  * exactly as fp4kv_kv_quant_fp4 does (packed / scales, nullable with kv_out given).
  * q         : nullable bf16; head h of token i at q + i * q_tok_stride + h * q_head_stride.

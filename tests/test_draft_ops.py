@@ -404,6 +404,34 @@ def test_norm_rope_rows_that_are_not_finite(fk, n, d):
 
 
 @gpu
+@pytest.mark.parametrize("rope, half", [(0, False), (64, False), (64, True)])
+@pytest.mark.parametrize("n, H, d", [(3, 5, 512), (700, 64, 512), (40, 7, 128), (20, 9, 1024)])
+def test_norm_rope_queries_that_are_not_finite(fk, n, H, d, rope, half):
+    """By the formula, as for KV rows: NaN makes its head NaN; an infinity makes r 0, so NaN in its own place (and,
+    rotated, in its partner's) and zeros elsewhere. The other heads are as without."""
+    q = torch.randn(n, H, d, generator=gen(75), device=DEV).bfloat16()
+    w = (1 + 0.2 * torch.randn(d, generator=gen(76), device=DEV)).bfloat16()
+    table, pos = (table_of(64, rope), torch.arange(n, device=DEV) % 64) if rope else (None, None)
+    x = q.clone()
+    x[0, 0, 3] = float("nan")
+    x[0, 1, 0] = float("inf")         # (its neighbour is not rotated with it)
+    x[1, 2, d - 65] = float("-inf")
+    x[n - 1, H - 1, 17] = float("inf")
+    x[2, 0, d - 1] = float("-inf")    # rotated, if any is, with channel d - 2, or d - 1 - rope / 2
+    how = dict(positions=pos, cos_sin=table, rope_dim=rope, rope_half=half, q_weight=w)
+    want, got = fk.qkv_norm_rope_fp4(q, None, **how)[0], fk.qkv_norm_rope_fp4(x, None, **how)[0]
+    hit = torch.zeros(n, H, dtype=torch.bool, device=DEV)
+    for t, h, places in ((0, 0, range(d)), (0, 1, [0]), (1, 2, [d - 65]), (n - 1, H - 1, [17]),
+                         (2, 0, [d - 1] + ([d - 1 - rope // 2 if half else d - 2] if rope else []))):
+        hit[t, h] = True
+        nan = torch.zeros(d, dtype=torch.bool, device=DEV)
+        nan[list(places)] = True
+        assert torch.equal(torch.isnan(got[t, h]), nan), (t, h, torch.isnan(got[t, h]).nonzero().tolist())
+        assert (got[t, h][~nan] == 0).all()
+    assert torch.equal(got[~hit], want[~hit])
+
+
+@gpu
 @pytest.mark.parametrize("half", [False, True])
 def test_norm_rope_rows_near_the_ends_of_the_type(fk, half):
     """r below fp32's normal range (channels near 3e38), and rows of tiny channels: kv_out is exact."""
