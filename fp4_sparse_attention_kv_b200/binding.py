@@ -45,6 +45,7 @@ SIGNATURES = [
      [_P, _P, _I32, _P, _I32, _P, _I64, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _P]),
     ("fp4kv_profile_enable", ctypes.c_int, [_I32]),
     ("fp4kv_profile_read", ctypes.c_int, [ctypes.POINTER(_I32), ctypes.POINTER(_F32)]),
+    ("fp4kv_profile_read_kinds", ctypes.c_int, [_I32, ctypes.POINTER(_I32), ctypes.POINTER(_F32)]),
     ("fp4kv_selftest_wait_timeout", ctypes.c_int, [_I32, _P, _SZ, _P]),
     ("fp4kv_sparse_swa_attn_decode", ctypes.c_int,
      [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _I32, _P, _I32, _F32, _P, _P, _P, _SZ, _P]),
@@ -61,7 +62,7 @@ SIGNATURES = [
     ("fp4kv_selftest_wait_timeout_noalloc", ctypes.c_int, [_I32, _P]),
 ]
 
-KERNEL_KINDS = ("kv_quant_fp4", "index_score", "topk_select", "sparse_attn")
+KERNEL_KINDS = ("kv_quant_fp4", "index_score", "topk_select", "sparse_attn", "qkv_norm_rope_fp4", "kv_dequant_fp4", "tree_attn")
 
 
 class Fp4kvError(RuntimeError):
@@ -563,10 +564,11 @@ def profile_enable(on: bool = True):
 
 def profile_read() -> dict:
     """{kernel kind: (launches, total device ms)} since the last read; clears the records."""
-    n = (ctypes.c_int32 * 4)()
-    ms = (ctypes.c_float * 4)()
-    _check(lib().fp4kv_profile_read(n, ms))
-    return {KERNEL_KINDS[i]: (int(n[i]), float(ms[i])) for i in range(4)}
+    k = len(KERNEL_KINDS)
+    n = (ctypes.c_int32 * k)()
+    ms = (ctypes.c_float * k)()
+    _check(lib().fp4kv_profile_read_kinds(k, n, ms))
+    return {KERNEL_KINDS[i]: (int(n[i]), float(ms[i])) for i in range(k)}
 
 
 def indexer_topk_noalloc(q, w, keys, seq_lens, top_k, pool=None, block_size=8, key_scale=None,

@@ -55,9 +55,10 @@ int num_sms() {
 // Optional per-kernel timing for benchmarks: launches bracketed by CUDA events.
 // ---------------------------------------------------------------------------------------
 namespace prof {
-constexpr int kKinds = 4;  // 0 kv_quant, 1 indexer scoring, 2 top-K select, 3 sparse attention
+// 0 kv_quant, 1 indexer scoring, 2 top-K select, 3 sparse attention (what fp4kv_profile_read gives),
+// 4 norm-rotate-write, 5 read-back, 6 tree attention
 struct Rec {
-  int kind;
+  int kind, launches;
   cudaEvent_t a, b;
 };
 std::mutex mu;
@@ -77,10 +78,10 @@ cudaEvent_t take() {
 }
 
 struct Scope {
-  int kind;
+  int kind, launches;
   cudaStream_t s;
   cudaEvent_t a = nullptr;
-  Scope(int k, cudaStream_t st) : kind(k), s(st) {
+  Scope(int k, cudaStream_t st, int n = 1) : kind(k), launches(n), s(st) {
     std::lock_guard<std::mutex> g(mu);
     if (!enabled) return;
     a = take();
@@ -92,7 +93,7 @@ struct Scope {
     cudaEvent_t b = take();
     if (!b) return;
     cudaEventRecord(b, s);
-    recs.push_back({kind, a, b});
+    recs.push_back({kind, launches, a, b});
   }
 };
 }  // namespace prof
@@ -667,7 +668,7 @@ fp4kv_status fp4kv_qkv_norm_rope_fp4(const uint16_t* q, int64_t q_tok_stride, in
   p.eps = eps;
   cudaError_t e;
   {
-    prof::Scope ps(0, static_cast<cudaStream_t>(stream));
+    prof::Scope ps(4, static_cast<cudaStream_t>(stream));
     e = fp4kv::launch_qkv_norm_rope(p, num_sms(), static_cast<cudaStream_t>(stream));
   }
   if (e != cudaSuccess) return cuda_fail(e, "qkv_norm_rope_fp4");
@@ -688,7 +689,7 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
   if (!src_row && n_rows > cap_rows) return fail(FP4KV_ERR_INVALID_ARG, "n_rows > cap_rows with src_row == NULL");
   cudaError_t e;
   {
-    prof::Scope ps(0, static_cast<cudaStream_t>(stream));
+    prof::Scope ps(5, static_cast<cudaStream_t>(stream));
     e = fp4kv::launch_kv_dequant_fp4(packed, scales, cap_rows, d, src_row, n_rows, out, out_f32 != 0, out_row_stride,
                                      num_sms(), static_cast<cudaStream_t>(stream));
   }
@@ -747,7 +748,7 @@ fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int
   p.status = reinterpret_cast<uint32_t*>(base);
   cudaError_t e;
   {
-    prof::Scope ps(3, static_cast<cudaStream_t>(stream));
+    prof::Scope ps(6, static_cast<cudaStream_t>(stream), p.whole ? 1 : 2);  // (parts are joined by a second kernel)
     e = fp4kv::launch_tree_attn(p, static_cast<cudaStream_t>(stream));
   }
   if (e != cudaSuccess) return cuda_fail(e, "tree_attn_decode");
@@ -881,13 +882,18 @@ fp4kv_status fp4kv_profile_enable(int32_t on) {
 }
 
 fp4kv_status fp4kv_profile_read(int32_t* launches, float* total_ms) {
+  return fp4kv_profile_read_kinds(4, launches, total_ms);
+}
+
+fp4kv_status fp4kv_profile_read_kinds(int32_t n_kinds, int32_t* launches, float* total_ms) {
   if (!launches || !total_ms) return fail(FP4KV_ERR_INVALID_ARG, "null output arrays");
+  if (n_kinds < 1) return fail(FP4KV_ERR_INVALID_ARG, "n_kinds=%d", n_kinds);
   std::vector<prof::Rec> recs;
   {
     std::lock_guard<std::mutex> g(prof::mu);
     recs.swap(prof::recs);
   }
-  for (int k = 0; k < prof::kKinds; ++k) {
+  for (int k = 0; k < n_kinds; ++k) {
     launches[k] = 0;
     total_ms[k] = 0.0f;
   }
@@ -898,8 +904,8 @@ fp4kv_status fp4kv_profile_read(int32_t* launches, float* total_ms) {
     if (e == cudaSuccess) e = cudaEventElapsedTime(&ms, r.a, r.b);
     if (e != cudaSuccess) {
       err = e;
-    } else if (r.kind >= 0 && r.kind < prof::kKinds) {
-      launches[r.kind] += 1;
+    } else if (r.kind < n_kinds) {
+      launches[r.kind] += r.launches;
       total_ms[r.kind] += ms;
     }
   }

@@ -372,12 +372,14 @@ fp4kv_status fp4kv_selftest_wait_timeout_noalloc(int32_t limit_us, void* stream)
 /* Benchmark support (no counterpart on the pages). While enabled, every kernel the library
  * launches is bracketed by two CUDA events recorded on the launch stream (do not enable
  * during CUDA-graph capture). fp4kv_profile_read waits for the recorded events and returns,
- * per kernel kind [0 kv_quant (and the norm-rotate-write and read-back passes), 1 indexer
- * scoring, 2 top-K select, 3 sparse attention (and the tree attention)], the
+ * per kernel kind [0 kv_quant, 1 indexer scoring, 2 top-K select, 3 sparse attention], the
  * number of launches and their summed device time in milliseconds (host arrays of 4), then
- * clears the records. */
+ * clears the records. fp4kv_profile_read_kinds does the same for the first n_kinds kinds
+ * [4 norm-rotate-write, 5 read-back, 6 tree attention (with the kernel that joins its parts:
+ * two launches, one bracket)]; kinds behind n_kinds are cleared too. */
 fp4kv_status fp4kv_profile_enable(int32_t on);
 fp4kv_status fp4kv_profile_read(int32_t* launches, float* total_ms);
+fp4kv_status fp4kv_profile_read_kinds(int32_t n_kinds, int32_t* launches, float* total_ms);
 
 #ifdef __cplusplus
 }

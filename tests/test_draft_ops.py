@@ -1176,3 +1176,41 @@ def test_one_workspace_for_several_ops(fk):
             for got, ref in ((tree(None, ws), dense), (tree(idx, ws), chosen), (sparse(idx, ws), one), (tree(None, ws), dense)):
                 assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
     assert fk.workspace_status(ws) == 0
+
+
+def test_profile_refuses_no_arrays_and_no_kinds():
+    n, ms = (ctypes.c_int32 * 7)(), (ctypes.c_float * 7)()
+    for args, word in (((7, None, ms), "null"), ((7, n, None), "null"), ((0, n, ms), "n_kinds"), ((-1, n, ms), "n_kinds")):
+        st, msg = _c("fp4kv_profile_read_kinds", *args)
+        assert st == 1 and word in msg
+    assert _c("fp4kv_profile_read_kinds", 9, (ctypes.c_int32 * 9)(), (ctypes.c_float * 9)())[0] == 0
+
+
+@gpu
+def test_profile_counts_each_operator_by_itself(fk):
+    n, H = 900, 64
+    packed, scales = make_cache(fk, 1, n, 170)
+    x = torch.randn(n, 512, generator=gen(171), device=DEV).bfloat16()
+    q = torch.randn(1, 1, H, 512, generator=gen(172), device=DEV).bfloat16()
+    lens, mask = torch.tensor([n - 1], dtype=torch.int32, device=DEV), torch.ones(1, 1, dtype=torch.int64, device=DEV)
+    short = packed[:, :100].contiguous(), scales[:, :100].contiguous()
+    idx = torch.arange(64, dtype=torch.int32, device=DEV).view(1, -1)
+    fk.profile_read()
+    fk.profile_enable(True)
+    try:
+        fk.kv_quant_fp4(x, packed[0], scales[0])
+        for _ in range(2):
+            fk.qkv_norm_rope_fp4(None, x, packed=packed, scales=scales)
+        for _ in range(3):
+            fk.kv_dequant_fp4(packed, scales)
+        fk.sparse_attn_decode(q[:, 0], packed, scales, lens, idx)
+        fk.tree_attn_decode(q, packed, scales, lens, mask)           # parts, and the kernel that joins them
+        fk.tree_attn_decode(q, *short, lens.clamp(max=99), mask)     # whole items
+    finally:
+        fk.profile_enable(False)
+    got = fk.profile_read()
+    counts = {k: c for k, (c, _) in got.items()}
+    assert counts == {"kv_quant_fp4": 1, "index_score": 0, "topk_select": 0, "sparse_attn": 1, "qkv_norm_rope_fp4": 2,
+                      "kv_dequant_fp4": 3, "tree_attn": 3}, counts
+    assert all((ms > 0) == (c > 0) for c, ms in got.values())
+    assert all(c == 0 for c, _ in fk.profile_read().values())
