@@ -254,13 +254,14 @@ FP4KV_DEV Seq seq_of(const TreeAttnParams& p, int b) {
 // Clusters in use for `total` tiles of `items` items, whose tiles are `tiles` each (0: not all the same):
 // at least min_tiles each. Where whole fractions of an item to a cluster cost no more than the parts
 // that begin and end anywhere, they are taken: a cluster then has one segment, not two, and a segment costs
-// about as much as 8 tiles (Q, the pipeline's start, the output). With fractions and without: 32 items of 33
-// tiles 42.1 and 46.3 us, 16 of 63 41.0 and 44.3, 32 of 63 58.4 and 59.4, 8 of 313 66.1 and 70.2.
+// about as much as 6 tiles (Q, the pipeline's start, the output). With fractions and without: 32 items of 33
+// tiles 51.2 and 56.3 us, 16 of 63 50.6 and 54.3, 32 of 63 72.8 and 75.5, 8 of 313 83.6 and 85.3; where they are
+// not taken, 16 of 200 100.3 and 98.0, 20 of 100 76.0 and 74.5, 30 of 150 133 and 123.
 FP4KV_DEV uint32_t clusters_used(uint32_t total, uint32_t items, uint32_t tiles, uint32_t n_clusters, uint32_t min_tiles) {
   const uint32_t n = max(1u, min(n_clusters, total / min_tiles + (total % min_tiles != 0)));
   if (tiles == 0 || items > n) return n;
   const uint32_t k = n / items;  // clusters an item
-  return (tiles + k - 1) / k <= total / n + 8 ? k * items : n;
+  return (tiles + k - 1) / k <= total / n + 6 ? k * items : n;
 }
 // floor(total * i / used): where cluster i's range starts.
 FP4KV_DEV uint32_t range_start(uint32_t total, uint32_t used, uint32_t i) {
@@ -1134,23 +1135,33 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeAttnParams p) {
 
 int tree_min_tiles() { return 2; }
 
-// Items go whole to a cluster where sharing them would save less than it costs. A segment costs what
-// kSegment tiles do beside its own, so whole items take ceil(items / clusters) (tiles + kSegment); sharing
-// levels that to items / clusters, for one more segment per cluster and the second launch: 17 tiles together.
-// Items of more than 20 tiles are always shared (their real lengths, which the host doesn't know, may
-// differ). 64 heads, whole against shared: 4 items of 8 tiles 22.5 against 22.8 us, of 15 30.9 against
-// 25.0; 16 items of 5 19.8 against 23.8; 96 items of 9 42.0 against 51.0, of 15 55.8 against 61.1, of 22 72.6
-// against 71.1; 128 items of 8 40.5 against 58.4.
-constexpr int64_t kSegment = 8, kSharing = 17, kMostWhole = 20;
+// Items go whole to a cluster where sharing them would save less than it costs. All of them at once (up to one
+// a cluster): an item shared by k clusters is done t - t / k tiles sooner, and the kernel that joins the parts takes
+// as long as kJoin tiles. In several turns: a segment costs what kSegment tiles do beside its own, so whole items
+// take ceil(items / clusters) (t + kSegment); sharing levels that to items / clusters, for one more segment per
+// cluster and the second launch, kSharing tiles together. t counts the cache's rows, or the selection's, and 64
+// drafts. Items of more than 20 tiles are always shared (their real lengths, which the host doesn't know, may
+// differ). With 64 heads and 2 drafts (so of one tile less than t), whole against shared: 4 items of 5 tiles 23.9
+// against 26.1 us, of 8 28.7 against 26.3, of 15 39.6 against 29.1; 16 of 5 25.3 against 28.4, of 8 29.2 against
+// 28.3; 37 of 9 32.6 against 32.9, of 18 46.0 against 40.6; 45 of 20 49.0 against 52.3; 75 of 9 49.8 against 53.3,
+// of 15 69.1 against 62.8; 96 of 9 53.6 against 63.1, of 15 71.9 against 76.9, of 22 91.2 against 90.2; 128 of 8
+// 52.2 against 69.3; 225 of 12 112 against 118.
+constexpr int64_t kJoin = 5, kSegment = 6, kSharing = 19, kMostWhole = 20;
 static_assert(kMostWhole < int64_t(kFlush) && kFlush % 2 == 0, "whole items have no workspace; one set flushes");
+static_assert(kJoin + 1 + kSegment <= kSharing, "items of kJoin + 1 tiles are whole in several turns too");
 static int64_t tree_item_tiles(int64_t cap, int64_t top_k) { return ((top_k ? top_k : cap) + 64 + kTile - 1) / kTile; }
 
-bool tree_always_whole(int64_t cap, int64_t top_k) { return tree_item_tiles(cap, top_k) + kSegment <= kSharing; }
+bool tree_always_whole(int64_t cap, int64_t top_k) { return tree_item_tiles(cap, top_k) - 1 <= kJoin; }
 
 bool tree_whole_items(int64_t B, int64_t rows, int64_t cap, int64_t top_k, int num_sms) {
   const int64_t t = tree_item_tiles(cap, top_k), items = B * ((rows + kRows - 1) / kRows), most = num_sms / 2;
+  if (t > kMostWhole) return false;
+  if (items <= most) {
+    const int64_t k = most / items;
+    return t - (t + k - 1) / k <= kJoin;
+  }
   const int64_t idle = (most - items % most) % most;  // clusters without an item in the last turn
-  return tree_always_whole(cap, top_k) || (t <= kMostWhole && idle * (t + kSegment) <= kSharing * most);
+  return idle * (t + kSegment) <= kSharing * most;
 }
 
 int64_t tree_tiles(int64_t B, int64_t rows, int64_t cap, int64_t top_k) {
