@@ -87,8 +87,9 @@ typedef enum {
 
 /* Supported ranges (anything else returns FP4KV_ERR_UNSUPPORTED):
  *   d % 32 == 0 and 32 <= d <= 1024 (attention: d == 512);   indexer key dim == 128;
- *   1 <= H_I <= 64;   1 <= top_k <= 4096;   1 <= H <= 128;   1 <= block_size, and
- *   block_size == 8 for the pool;   1 <= n_pool_blocks <= 4096;   1 <= B <= 65535.       */
+ *   1 <= H_I <= 64;   1 <= top_k <= 4096 (tree attention: 2^20);   1 <= H <= 128;
+ *   1 <= block_size, and block_size == 8 for the pool;   1 <= n_pool_blocks <= 4096;
+ *   1 <= B <= 65535;   1 <= T <= 64 drafted tokens.                                      */
 
 /* Text of the last error raised on the calling thread ("" after a successful call). */
 const char* fp4kv_last_error(void);
