@@ -31,9 +31,7 @@ FP4KV_DEV void store_32b(uint8_t* at, const uint32_t* w, bool al32) {
 }
 // Eight codes times a scale -> four f16x2.
 FP4KV_DEV void values8(uint32_t codes, uint32_t s2, uint32_t (&h)[4]) {
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(codes));
+  e2m1x8_to_f16(codes, h);
 #pragma unroll
   for (int k = 0; k < 4; ++k) h[k] = hmul2_f16(h[k], s2);
 }

@@ -53,23 +53,6 @@ FP4KV_DEV float half_of(uint32_t w, int k) {  // channel k (0 low, 1 high) of a 
 }
 FP4KV_DEV uint4 ld_v4(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// two fp32 at once
-FP4KV_DEV uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-FP4KV_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-FP4KV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-FP4KV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 FP4KV_DEV uint64_t widen2(uint32_t w) { return pack2(half_of(w, 0), half_of(w, 1)); }
 
 // The 8-channel unit that holds the partners of the unit at channel c0 (pairs of halves), and whether c0's
@@ -83,17 +66,9 @@ FP4KV_DEV int partner_unit(const NormRopeParams& p, int c0, bool& second) {
 // ---------------------------------------------------------------------------------------
 // queries
 // ---------------------------------------------------------------------------------------
-FP4KV_DEV void cp_async_16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 FP4KV_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 FP4KV_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-FP4KV_DEV uint4 lds_v4(uint32_t at) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-  return r;
-}
 
 template <int LPR, int GPL, int kPairs>
 FP4KV_DEV void query_heads(const NormRopeParams& p, uint32_t ring, int64_t tok, int h0, int h1) {

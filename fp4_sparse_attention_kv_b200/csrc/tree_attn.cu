@@ -137,35 +137,9 @@ FP4KV_DEV void st_async_f32(uint32_t dst, float v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(dst), "f"(v), "r"(bar) : "memory");
 }
 
-FP4KV_DEV void cp_async_16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-FP4KV_DEV uint4 lds_v4(uint32_t at) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-  return r;
-}
 FP4KV_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 FP4KV_DEV void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-
-// two fp32 at once
-FP4KV_DEV uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-FP4KV_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-FP4KV_DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-FP4KV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // One lane of a converged warp.
 FP4KV_DEV uint32_t elect_lane() {
@@ -330,12 +304,6 @@ FP4KV_DEV void ld_nc_32b(uint32_t (&r)[8], const uint8_t* p, bool al32) {
 // Four E4M3 scales, a NaN (all bits but the sign) as 1.875.
 FP4KV_DEV uint32_t finite_scales(uint32_t s) {
   return s & ~((((s & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 1);
-}
-// Eight codes -> four f16x2 (the byte registers spare the shifts).
-FP4KV_DEV void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 // A chunk's row in shared memory, by lane j = 0 .. 3 of the four that share a row: unit k of 16 bytes goes to
 // position k ^ (row & 7) (the swizzle), and the lane writes its units in the order k ^ 2 j. That way a
