@@ -1214,3 +1214,44 @@ def test_profile_counts_each_operator_by_itself(fk):
                       "kv_dequant_fp4": 3, "tree_attn": 3}, counts
     assert all((ms > 0) == (c > 0) for c, ms in got.values())
     assert all(c == 0 for c, _ in fk.profile_read().values())
+
+
+@gpu
+@pytest.mark.parametrize("B, T, H, cap, every", [(65535, 1, 2, 4, 3), (65535, 2, 1, 3, 1), (4096, 2, 64, 1400, 700)])  # (whole items twice, parts)
+def test_tree_batches_of_many_sequences(fk, B, T, H, cap, every):
+    """The largest batch, and one in which every 700th sequence alone drafts: against the plain form of all at once.
+    Beside what test_tree_rows_that_cancel counts, fp16's least step: a probability's two parts are rounded to
+    2^-24 below 2^-14, 2^-25 each, where the row's largest is at least 2^7: 2^-31 sum |v|."""
+    g = gen(180)
+    packed = torch.randint(0, 256, (B, cap, 256), generator=g, device=DEV).to(torch.uint8)
+    scales = torch.randint(0x30, 0x40, (B, cap, 32), generator=g, device=DEV).to(torch.uint8)
+    q = torch.randn(B, T, H, 512, generator=g, device=DEV).bfloat16()
+    lens = torch.randint(0, cap + 2, (B,), generator=g, device=DEV).int()
+    mask = torch.randint(0, 1 << T, (B, T), generator=g, device=DEV)
+    drafts = torch.randint(0, T + 1, (B,), generator=g, device=DEV).int()
+    drafts[torch.arange(B, device=DEV) % every != every - 1] = 0
+    out, lse = torch.full_like(q, 3.0), torch.full((B, T, H), 5.0, device=DEV)
+    fk.tree_attn_decode(q, packed, scales, lens, mask, n_draft=drafts, sm_scale=0.04, out=out, lse=lse)
+    live = torch.arange(T, device=DEV) < drafts[:, None]
+    assert (out[~live] == 3.0).all() and (lse[~live] == 5.0).all()
+    rows = drafts.nonzero()[:, 0]
+    step = max(1, 30_000 // cap)
+    pos = torch.arange(cap, device=DEV)
+    for r in rows.split(step):
+        v = fk.kv_dequant_fp4(packed[r], scales[r], dtype=torch.float32).view(len(r), cap, 512).double()
+        n = lens[r].long().clamp(max=cap)[:, None, None]
+        j = pos - n
+        see = (j < 0) | ((j < drafts[r].long()[:, None, None]) & ((mask[r][:, :, None] >> j.clamp(0, 63)) & 1 == 1))
+        z = torch.einsum("bthc,bnc->bthn", q[r].double(), v) * float(np.float32(0.04))
+        dz = 2.0 ** -16 * 0.04 * torch.einsum("bthc,bnc->bthn", q[r].double().abs(), v.abs()).amax(-1, keepdim=True)
+        z = z.masked_fill(~see[:, :, None], -np.inf)
+        want_l = torch.logsumexp(z, -1)
+        p = torch.exp(z - want_l[..., None]).nan_to_num(0.0)  # (a token that sees nothing)
+        want, A = torch.einsum("bthn,bnc->bthc", p, v), torch.einsum("bthn,bnc->bthc", p, v.abs())
+        ok = live[r]
+        least = 2.0 ** -31 * v.abs().sum(1)[:, None, None]
+        off = (out[r].double() - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -16 + 2 * dz) * A + least)
+        assert (off[ok] <= 0).all()
+        inf = torch.isneginf(want_l)
+        assert torch.equal(torch.isneginf(lse[r])[ok], inf[ok])
+        assert ((lse[r].double() - want_l).abs() <= dz[..., 0] + 2.0 ** -20 * (1 + want_l.abs()))[ok[..., None] & ~inf].all()
