@@ -8,7 +8,7 @@
 // channels in bf16, 16 in fp32) from one load of codes, written as two 32-byte sectors: addresses
 // and row numbers cost more instructions than the values where it makes 16 bytes (65,536 rows of 512 to
 // bf16 out of a cache of 1,048,576: 20 us that way, 16 us
-// this way, 5.5 TB/s; 400,000 rows in order to fp32: 140 us, 6.7 TB/s). A block owns whole rows, so that the row of a unit
+// this way, 5.5 TB/s; 400,000 rows in order to fp32: 142 us, 6.6 TB/s). A block owns whole rows, so that the row of a unit
 // comes from a 32-bit division by a small number (a multiply and a shift).
 #include "fp4kv_common.cuh"
 #include "fp4kv_launch.h"
@@ -131,9 +131,11 @@ cudaError_t launch_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
                                   const int64_t* src_row, int64_t n_rows, void* out, bool f32, int64_t out_row_stride,
                                   int num_sms, cudaStream_t stream) {
   if (n_rows == 0) return cudaSuccess;
-  // Two units per thread, whose loads overlap, where one unit each would be more than the threads that fit;
-  // one where latency counts. Gathered rows of 512, one against two units: 16,384 to bf16 6.2 against 6.5 us,
-  // to fp32 8.3 against 6.8, 37,888 to bf16 10.0 against 7.8, 65,536 14.5 against 13.0.
+  // Two units per thread, whose loads overlap, and a dependent launch where one unit each would be more than the
+  // threads that fit; one, launched plainly, below: there the host's 6 to 7 us a call are what counts. Rows of 512
+  // gathered from 1,048,576 (neither they nor the output in L2, calls replayed from a graph), one unit launched plainly
+  // against two: 9,472 to bf16 4.5 against 4.2 us, to fp32 5.9 against 5.4, 18,944 to bf16 6.5 against 5.9, to fp32 9.9
+  // against 8.8, 37,888 to bf16 10.8 against 9.7, 65,536 16.8 against 15.7.
   const int64_t units = n_rows * (d / (f32 ? 16 : 32));
   const bool big = units > int64_t(num_sms) * 8 * kThreads;
   if (f32)

@@ -13,7 +13,7 @@
 // token, every channel is y = (x P + x_partner Q) r, two at a time in packed fp32 (outside the rotated
 // channels P = w, Q = 0), so no lane waits for the rotated ones. fp32, rounded once to bf16. Rows come
 // through a ring in shared memory, four passes ahead (in registers one ahead fitted: 241 us for 8,192
-// tokens of 64 heads; now 185 us, 5.9 TB/s).
+// tokens of 64 heads with their KV rows and a read table of positions; now 185 us, 5.9 TB/s; the queries alone 170).
 //
 // The KV row: y's nearest fp32 value is rounded to bf16 and that is quantised, so the cache holds
 // exactly what kv_quant_fp4 makes of kv_out. A code is decided by which side of a border a value
@@ -23,7 +23,7 @@
 // lies nearer than that (6, or 3 units) to a bf16 rounding border, y is formed in fp64: one value in
 // thousands. The rotated groups of a warp's rows are done together, one to a lane, after the others
 // (beside the others four lanes in 32 worked on them: 1,150 instructions a row, 172 us for 131,072 rows;
-// now 532 and 93 us, bound by issuing them).
+// now 532 and 98 us, bound by issuing them).
 #include "fp4kv_common.cuh"
 #include "fp4kv_launch.h"
 #include "fp4kv_quant.cuh"
@@ -436,9 +436,9 @@ FP4KV_DEV void kv_rows(const NormRopeParams& p, int64_t row0) {
 }
 
 // Rows of a KV warp: eight (four of more than 512 channels), whose rotated groups share the lanes and whose
-// loads overlap; where that leaves SMs without a warp or two, as few as a pass has. Rows of 512, one pass
-// against eight: 1,024 rows 8.3 against 9.0 us, 4,096 10.6 against 9.2, 9,472 16.5 against 10.1, 131,072 170
-// against 93.
+// loads overlap; where that leaves SMs without a warp or two, as few as a pass has. Rows of 512 (not in L2, calls
+// replayed from a graph), one pass against eight: 1,024 rows 5.1 against 9.7 us, 4,096 12.6 against 11.6, 9,472
+// 23.2 against 12.0, 131,072 286 against 98.
 template <int LPR, int GPL>
 constexpr int kKvPasses = (GPL == 1 ? 8 : 4) * LPR / 32;
 
@@ -491,8 +491,8 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   }
   // Heads per warp: one pass (kRows) where there are few rows, up to 16 passes where that leaves every SM
   // 8 warps (as many as its ring of rows needs, and the coefficients are formed once for all of them). 64
-  // heads of 512, 1, 4 and 16 a warp: 32 tokens 8.3, 7.6, 8.0 us (the host's time), 128 tokens 10.4, 7.5, 8.2, 512
-  // tokens 30.8, 14.5, 11.6, 8,192 tokens 507, 222, 166.
+  // heads of 512 without KV rows (not in L2, calls replayed from a graph), 1, 4 and 16 a warp: 32 tokens 4.3, 5.1,
+  // 8.9 us, 128 tokens 12.0, 7.1, 9.6, 512 tokens 37.3, 18.7, 14.9, 8,192 tokens 554, 237, 170.
   int heads = kRows;
   while (heads < 16 * kRows && heads < p.H && p.n_tokens * p.H >= int64_t(2) * heads * 8 * num_sms) heads *= 2;
   const int64_t units = p.n_tokens * ((p.H + heads - 1) / heads);
