@@ -16,10 +16,10 @@
 // dequantize the tile's rows for themselves. Tensor work is 1,024 cycles a tile for the scores, 2,048 for the values.
 // (Splitting the channels instead, each CTA with half of q, V and O, needs S summed over the two CTAs:
 // 24 KiB a tile each way and a round trip, and took 2,850 cycles a tile, with P in one part. P in one part took
-// 2,030 cycles a tile in this form, in two it takes 2,370.)
-// 4 x 1,024 query rows over 32,784 rows each: 340 us, bound by the values' tensor work (86 % of a tile's cycles, at
-// the 1.6 GHz that the power limit leaves). 8 x 512 over 2,056: 52 us, 32 x 320 over 517: 46 us, bound by an item's
-// start and end.
+// 2,100 cycles a tile in this form, in two it takes 2,465.)
+// 4 x 1,024 query rows over 32,784 rows each: 348 to 372 us (1.84 to 1.6 GHz: the power limit), bound by the value
+// CTA: its tensor core works 83 % of a tile's cycles, and reads 1,536 wavefronts of operands a tile beside the
+// dequantization's stores. 8 x 512 over 2,056: 51 us, 32 x 320 over 517: 45 us, bound by an item's start and end.
 //
 // A CTA (28 warps):
 //  * warps 16-23 dequantize a tile's 64 rows to fp16 (exact) in 128-byte-swizzled 64-channel chunks,
@@ -59,7 +59,8 @@ constexpr int kPSlots = 2;  // tiles of P: tile m's in slot m & 1
 // Tiles that are added up in TMEM at most. The tensor core's fp32 sums are cut off, not rounded: each of the 8
 // steps of a tile loses half an ulp of O on average, always towards zero (2^-14 after 256 tiles; 2^-8 after 16,384). After
 // kFlush tiles of an item O goes to the workspace, where it is added with rounding, and starts again from zero; a row's
-// sum is kept in as many parts. Costs 3 % from 512 tiles on (661 against 643 us for 8,192 query rows over 32,832);
+// sum is kept in as many parts. Costs 3 % from 512 tiles on (661 against 643 us for 8,192 query rows over 32,832; with
+// 64 tiles 16 %);
 // without it a prefix of 1,000,000 rows came out 0.4 to 0.8 % too small.
 constexpr uint32_t kFlush = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
