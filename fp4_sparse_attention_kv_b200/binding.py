@@ -505,7 +505,7 @@ def tree_attn_decode(q, packed, scales, prefix_lens, tree_mask, *, n_draft=None,
     512]; packed uint8 [B, cap, 256]; scales uint8 [B, cap, 32]; prefix_lens int32 [B];
     tree_mask int64 [B, T] (bit j: the token sees draft j, whose row is prefix_lens + j);
     n_draft (optional) int32 [B]; idx (optional) int32 [B, top_k], top_k >= 1: the prefix positions to
-    attend (every one without it; rows of -1: none). Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
+    attend (every one without it; rows of -1: none); sm_scale: finite. Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H] or
     None); tokens behind n_draft keep what their outputs held."""
     if idx is not None and (idx.dim() != 2 or idx.shape[1] < 1):
         # (the address of no entries is null, which the library takes for no selection)

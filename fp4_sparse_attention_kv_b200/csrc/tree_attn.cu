@@ -32,10 +32,11 @@
 // in fp16, S and O in fp32. A row's logits are c S (log2 domain). The reference m, a value of S, moves only when a
 // logit passes it by 2^8, to the maximum; p = 2^(c (S - m) + 7). The difference comes first: c S and c m rounded
 // apart, a row's largest p could be anything once a logit has no bits left below 1 (from 2^24 on). c is cut off at
-// 2^90 there, where it multiplies the least difference of two S (2^-34) to 2^56: one row has it all either way. A row's
-// largest p is at least 2^7 and at most 2^15, and goes as two fp16: its upper 11 bits and the rest, rounded to 11 bits. Together they are off by at most 2^-21 of p, or by
-// 2^-24, 2^-31 of the largest. One fp16 alone, 2^-12, would show where rows cancel, and breaks the library's
-// bound on its attention (5e-3 in every value) where some rows are a hundred times louder. The sums are fp32.
+// 2^90 there, where it multiplies the least difference of two S (2^-34) to 2^56: one row has it all either way.
+// A row's largest p is at least 2^7 and at most 2^15. p goes as two fp16, its upper 11 bits and the rest rounded
+// to 11 bits: together off by at most 2^-21 of p, or by 2^-24, which is 2^-31 of the largest. One fp16 alone, 2^-11,
+// shows where rows cancel, and breaks the library's bound on its attention (5e-3 in every value) where some rows
+// are a hundred times louder. The sums are fp32.
 // Every wait is bounded; on timeout a status bit is set and the kernel winds down.
 #include <atomic>
 
@@ -57,11 +58,10 @@ constexpr int kStages = 2;  // tiles of V
 constexpr int kSlots = 4;   // tiles of S
 constexpr int kPSlots = 2;  // tiles of P: tile m's in slot m & 1
 // Tiles that are added up in TMEM at most. The tensor core's fp32 sums are cut off, not rounded: each of the 8
-// steps of a tile loses half an ulp of O on average, always towards zero (2^-14 after 256 tiles; 2^-8 after 16,384). After
-// kFlush tiles of an item O goes to the workspace, where it is added with rounding, and starts again from zero; a row's
-// sum is kept in as many parts. Costs 3 % from 512 tiles on (661 against 643 us for 8,192 query rows over 32,832; with
-// 64 tiles 16 %);
-// without it a prefix of 1,000,000 rows came out 0.4 to 0.8 % too small.
+// steps of a tile loses half an ulp of O on average, always towards zero (2^-14 after 256 tiles; 2^-8 after 16,384).
+// After kFlush tiles of an item O goes to the workspace, where it is added with rounding, and starts again from zero;
+// a row's sum is kept in as many parts. Costs 3 % from 512 tiles on (661 against 643 us for 8,192 query rows over
+// 32,832; 64 tiles instead of 256 cost 16 %); without it a prefix of 1,000,000 rows came out 0.4 to 0.8 % too small.
 constexpr uint32_t kFlush = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMoveLog2 = 8.0f, kPLog2 = 7.0f;  // a reference moves past 2^8; p = 2^7 at it
@@ -90,8 +90,8 @@ static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kColS = 256;
 
 // Barriers. V's have two halves of 32 rows. Of S's slots: SFULL, SFREE (scores). Of P's: PXFULL, PREADY (values) and,
-// for either half, PFREE (O has it, in both). SEG: the last product of an item is complete. A wait goes by parity, so nobody may
-// wait for a use of a barrier before the use before it is known to be over.
+// for either half, PFREE (O has it, in both). SEG: the last product of an item is complete. A wait goes by parity, so
+// nobody may wait for a use of a barrier before the use before it is known to be over.
 enum { B_VFULL = 0, B_VFREE = 6, B_SFULL = 12, B_SFREE = 16, B_PFREE = 20, B_PXFULL = 24, B_PREADY = 26, B_REF = 32,
        B_QREADY = 34, B_SEG = 35, B_DONE = 36, B_COUNT = 37 };
 static_assert(8 * B_COUNT <= 320, "barriers");
@@ -167,7 +167,8 @@ FP4KV_DEV void umma_ss(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t
       " setp.ne.b32 g, %5, 0;\n @g tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}"
       ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(go), "n"(kAHigh), "n"(kBHigh) : "memory");
 }
-// High words of the 128-byte and 64-byte swizzled layouts: 1024 bytes between 8-row groups (P's high and low parts alternate).
+// High words of the 128-byte and 64-byte swizzled layouts: 1024 bytes between 8-row groups (of P's, high and low
+// parts alternate).
 constexpr uint32_t kHigh128 = (1024u >> 4) | (1u << 14) | (2u << 29), kHigh64 = (1024u >> 4) | (1u << 14) | (4u << 29);
 FP4KV_DEV void commit_if(uint32_t go, uint64_t* bar) {
   asm volatile(

@@ -312,7 +312,8 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  *     twice); and
  *   - the drafted rows j whose bit j of tree_mask[b][t] is set (its own bit included: a mask
  *     without it leaves the token's own row out).
- * q [B][T][H][512] bf16; out the same shape, bf16; lse (nullable) fp32 [B][T][H] as in
+ * q [B][T][H][512] bf16; out the same shape, rounded once to bf16 (what is rounded keeps to the
+ * bounds that fp4kv_sparse_attn_decode's output does); lse (nullable) fp32 [B][T][H] as in
  * fp4kv_sparse_attn_decode. packed [B][cap][256], scales [B][cap][32]. n_draft (nullable)
  * int32 [B]: sequence b drafts only its first n_draft[b] (clamped to [0, T]) tokens; q, mask
  * and outputs of the others are not touched, and mask bits at or above it are ignored. Prefix
