@@ -107,6 +107,9 @@ FP4KV_DEV uint32_t map_peer(uint32_t addr, uint32_t rank) {
 FP4KV_DEV void mbar_arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+FP4KV_DEV void st_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 FP4KV_DEV bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -523,10 +526,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   uint32_t seg = 0;  // segments so far
 
   auto aborted = [&]() { return __any_sync(0xffffffffu, *s_abort != 0) != 0; };
+  // (in both CTAs: neither may leave while the other's copies may still be on their way)
   auto give_up = [&]() {
     if (lane == 0) {
       atomicOr(p.status, kFlagWaitTimeout);
       *s_abort = 1;
+      st_peer_u32(map_peer(smem_u32(smem) + kOffMisc + 4, values ? 0 : 1), 1);
     }
   };
 
@@ -1028,6 +1033,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_tree_
   }
   tc_fence_before();
   cluster_sync_all();  // (no arrival or store is on its way to a CTA that has left)
+  // In a range that ran to its end every copy of P has been waited for. After a wait that ran out nobody may have: the
+  // last ones, sent before the barrier, get 1 ms (they take microseconds) before either end's shared memory goes.
+  if (*s_abort != 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
