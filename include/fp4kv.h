@@ -326,7 +326,8 @@ fp4kv_status fp4kv_kv_dequant_fp4(const uint8_t* packed, const uint8_t* scales, 
  * 1 <= T <= 64; 1 <= H <= 128; d == 512; top_k in [1, 2^20] with idx, 0 without;
  * B * ceil(T H / 128) * ceil((R + 64) / 64) < 2^32 with R = top_k or cap. ws: at least
  * fp4kv_workspace_bytes(FP4KV_OP_TREE_ATTN, B, cap, T * H, top_k, 0) bytes, 256-byte aligned,
- * initialised once (fp4kv_workspace_init says what an indexer op needs behind it). q, packed, scales and out 16-byte aligned. */
+ * initialised once (fp4kv_workspace_init says what an indexer op needs behind it). q, packed,
+ * scales and out 16-byte aligned. */
 fp4kv_status fp4kv_tree_attn_decode(const uint16_t* q, int32_t B, int32_t T, int32_t H, int32_t d,
                                     const uint8_t* packed, const uint8_t* scales, int64_t cap,
                                     const int32_t* prefix_lens, const int32_t* n_draft, const uint64_t* tree_mask,

@@ -14,6 +14,7 @@ Tolerances:
   probability to a relative 2^-11: fp16 has a step of 2^-24 below 2^-14, so a p that is stored as at
   least 2^3 at the row's maximum is off by up to 2^-25 / 2^3 = 2^-28 of that maximum (<= 1), which
   adds 2^-28 sum_j |v_j|.
+  (A probability goes as two fp16 by now and is nearer than that; test_tree_rows_that_cancel counts it.)
 """
 import ctypes
 
